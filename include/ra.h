@@ -88,13 +88,15 @@ typedef enum ra_status {
   RA_ERR_UNSUPPORTED = 2,  /* p > RA_MAX_RANKS, unknown op, RA_AVG on an integer type, algo or
                               flag not valid for the call */
   RA_ERR_ALIAS = 3,        /* two rank buffers overlap */
-  RA_ERR_MISALIGNED = 4,   /* a buffer does not start on a 16-byte boundary */
+  RA_ERR_MISALIGNED = 4,   /* a buffer does not start on a 16-byte boundary (row operators: on a
+                              boundary of its elements) */
   RA_ERR_HIP = 5,          /* a HIP runtime call failed (see ra_last_error) */
   RA_ERR_TIMEOUT = 6       /* a device-side wait exceeded its time budget */
 } ra_status;
 
 typedef enum ra_dtype {
-  RA_INT32 = 0, RA_FLOAT32 = 1, RA_BFLOAT16 = 2, RA_FLOAT16 = 3, RA_FLOAT64 = 4, RA_INT64 = 5
+  RA_INT32 = 0, RA_FLOAT32 = 1, RA_BFLOAT16 = 2, RA_FLOAT16 = 3, RA_FLOAT64 = 4, RA_INT64 = 5,
+  RA_FLOAT8_E4M3 = 6   /* outputs of ra_allreduce_rmsnorm only: 8 bits, 4 of exponent, no infinities */
 } ra_dtype;
 
 typedef enum ra_op { RA_SUM = 0, RA_MAX = 1, RA_AVG = 2 } ra_op;
@@ -390,6 +392,161 @@ int ra_stream_copy(void* dst, const void* src, int64_t bytes, hipStream_t stream
  */
 int ra_stream_copy_resident(void* dst, const void* src, int64_t bytes, int grid,
                             hipStream_t stream);
+
+/*
+ * Row operators
+ * -------------
+ * What a transformer whose layers are cut over the p ranks ("tensor parallel")
+ * does at the places where it folds the ranks' buffers: the sum of a sublayer's
+ * partial outputs goes into the residual stream and its norm, the embedding and
+ * the loss have a vocabulary cut over the ranks, and the gradients go the same
+ * way back.  Shared by the calls below:
+ *
+ *  rows    an array of `tokens` x `hidden` is contiguous, one token after the
+ *          other.  Arrays start on a boundary of their elements; calls whose
+ *          arrays all start on 16-byte boundaries and whose rows have a multiple
+ *          of 8 elements run faster kernels, with the same results.
+ *  vocabulary  cut over the ranks as ra_chunk_bounds(vocab, p) says.  At most
+ *          2^24 columns.  Pieces without a column may be NULL.
+ *  dtype   RA_FLOAT32, RA_BFLOAT16 or RA_FLOAT16 (others: RA_ERR_UNSUPPORTED).
+ *          Sums, norms and exponentials are computed in float32, and every
+ *          output is rounded once, to nearest even.  The ranks' partials are
+ *          added in rank order, 0 first, in float32 (not rounded every hop as
+ *          ra_allreduce does).
+ *  outs    a result that all ranks need: n pointers, each of which gets the whole
+ *          result; n = 1 for ranks that share one copy.
+ *  results do not depend on the stream, the GPU's load or the call's history:
+ *          there are no floating-point atomics.
+ *  overlap two arrays of a call may share memory only if neither is written, or
+ *          where a call says that one may be exactly the other (RA_ERR_ALIAS).
+ *  workspace  device memory of the caller's, 16-byte aligned, whose size the
+ *          matching ..._workspace call gives (host only; 0 where none is needed,
+ *          then NULL will do).  It is scratch: nothing is kept in it between
+ *          calls, and calls that may overlap need one each.  So do HIP graphs
+ *          whose replays may overlap.
+ *  The calls wait for nothing, allocate nothing and can be captured into HIP
+ *  graphs on any stream.  The current device has to be the stream's.
+ *  tokens == 0 is RA_OK and writes nothing but what a call says.
+ */
+
+/*
+ * ra_allreduce_rmsnorm -- the sum over the ranks, added to the residual stream and
+ * normalised by its root mean square, to every rank:
+ *     h = residual_in + sum_r bufs[r]
+ *     y = h / sqrt(mean(h^2) + eps) * weight          (mean over the hidden columns)
+ *   bufs          p arrays [tokens][hidden] of `dtype`, read.  p = 1 is a plain norm.
+ *   residual_in   [tokens][hidden] of residual_dtype (`dtype` or RA_FLOAT32), or
+ *                 NULL for zeros
+ *   residual_out  h, rounded to residual_dtype, or NULL.  May be residual_in.  y is
+ *                 computed from the unrounded h.
+ *   weight        [hidden] of `dtype`
+ *   outs          n_out (1..p) arrays for y, of out_dtype: `dtype`, where each may be
+ *                 one of bufs (the sum in place, as ra_allreduce leaves it), or
+ *                 RA_FLOAT8_E4M3
+ *   scales        8-bit outputs: n_out arrays [tokens][ceil(hidden / group)] float32
+ *                 (group = 0: [tokens]), else ignored.  y stands for q * scale with
+ *                 scale = max(max |y|, 2^-110) / 448 over the group, q = y / scale to
+ *                 nearest even.  A group that holds an infinity or a NaN gives NaN.
+ *   group         0, 32, 64 or 128 columns to a scale
+ *   rstd          1 / sqrt(mean(h^2) + eps), [tokens] float32, or NULL; the backward
+ *                 call wants it
+ *   eps           > 0 and finite, so that a row of zeros gives zeros
+ * hidden is at most 32768.
+ */
+int ra_allreduce_rmsnorm(void* const* bufs, int p, int64_t tokens, int64_t hidden, int dtype,
+                         const void* residual_in, void* residual_out, int residual_dtype,
+                         const void* weight, float eps, void* const* outs, int n_out,
+                         int out_dtype, float* const* scales, int group, float* rstd,
+                         hipStream_t stream);
+
+/*
+ * ra_allreduce_rmsnorm_backward -- the gradient of ra_allreduce_rmsnorm:
+ *     g = sum_r dys[r],  x = h * rstd
+ *     dh = dh_in + rstd * (weight g - x mean(weight g x)),   dweight = sum over tokens of g x
+ *   dys      p arrays [tokens][hidden] of `dtype`: the gradients of y, of which each
+ *            rank has a part (p = 1: the whole)
+ *   h, rstd  what the forward call left in residual_out (h_dtype: `dtype` or
+ *            RA_FLOAT32) and rstd
+ *   dh_in    the gradient of residual_out that comes along the stream, h_dtype, or NULL
+ *   dh       the gradient of residual_in, h_dtype.  May be dh_in.
+ *   dxs      n_dx (0..p) arrays of `dtype`: the gradient of the ranks' partials, which
+ *            is dh for each of them.  Each may be one of dys.
+ *   dweight  [hidden] float32, or NULL.  With tokens == 0 it gets zeros.  Its sum over
+ *            the tokens has a fixed order.
+ *   workspace  ra_rmsnorm_backward_workspace bytes where dweight is wanted
+ */
+int ra_allreduce_rmsnorm_backward(void* const* dys, int p, int64_t tokens, int64_t hidden,
+                                  int dtype, const void* h, int h_dtype, const float* rstd,
+                                  const void* weight, const void* dh_in, void* dh,
+                                  void* const* dxs, int n_dx, float* dweight, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
+int ra_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes);
+
+/*
+ * ra_cross_entropy -- softmax cross entropy of logits whose vocabulary is cut over
+ * the ranks, and its gradient in the same call:
+ *     lse = ln sum_j exp(x_j),  loss = lse - x_target
+ *     dx_j = grad_scale * dloss * (exp(x_j - lse) - [j = target])
+ *   logits   p arrays; rank r's is [tokens][its columns] of `dtype`
+ *   valid    1..vocab: columns from `valid` on are padding.  They are not read as
+ *            logits, and their gradient is zero.
+ *   targets  [tokens] of target_dtype (RA_INT32 or RA_INT64).  Below 0: a token
+ *            without a loss (loss 0, gradient zeros whatever its logits hold).  From
+ *            `valid` on: NaN for the token's loss and gradient.
+ *   loss, lse  [tokens] float32; either may be NULL
+ *   grads    p arrays like logits, or NULL for no gradient.  grads[r] may be
+ *            logits[r]: then the gradient takes the logits' place and neither they
+ *            nor the probabilities are kept.
+ *   dloss    [tokens] float32: the gradient of each token's loss; NULL: ones
+ * Logits of -inf are masked columns.  A token all of whose columns are -inf has
+ * lse = -inf, loss = +inf and a gradient of zeros.  A logit of +inf or NaN makes
+ * its token NaN.
+ */
+int ra_cross_entropy(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid,
+                     int dtype, const void* targets, int target_dtype, float* loss, float* lse,
+                     void* const* grads, const float* dloss, float grad_scale, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+int ra_cross_entropy_workspace(int64_t tokens, int64_t vocab, int p, int64_t* bytes);
+
+/*
+ * ra_cross_entropy_backward -- the gradient alone, from the logits and the lse that an
+ * earlier ra_cross_entropy gave: for a program that learns dloss only later.
+ * Arguments as above; grads[r] may be logits[r].
+ */
+int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_t vocab,
+                              int64_t valid, int dtype, const void* targets, int target_dtype,
+                              const float* lse, void* const* grads, const float* dloss,
+                              float grad_scale, hipStream_t stream);
+
+/*
+ * ra_embedding -- rows of a table whose vocabulary is cut over the ranks, to every
+ * rank: y_t = scale * table[id_t].  (Each rank looking up its own rows, zeros for
+ * the others, and an all-reduce give the same.)
+ *   tables   p arrays; rank r's is [its rows][hidden] of `dtype`
+ *   ids      [tokens] of id_dtype (RA_INT32 or RA_INT64).  Below 0: padding, a row of
+ *            zeros.  From vocab on: a row of NaN.
+ *   outs     n_out (1..p) arrays [tokens][hidden] of `dtype`
+ * hidden is at most 2^20.
+ */
+int ra_embedding(const void* const* tables, int p, int64_t vocab, int64_t hidden, int dtype,
+                 const void* ids, int id_dtype, int64_t tokens, float scale, void* const* outs,
+                 int n_out, hipStream_t stream);
+
+/*
+ * ra_embedding_backward -- the gradient of the tables: dtable[v] = scale * the sum of dy
+ * over the tokens with id v, added up in the order of their positions.
+ *   dy       [tokens][hidden] of `dtype`
+ *   dtables  p arrays like the tables, of dtable_dtype (`dtype` or RA_FLOAT32)
+ *   accumulate  0: every row is written, zeros where no token has it (with tokens ==
+ *            0 too).  1: the rows that tokens have are added to, others left alone.
+ *   ids outside 0..vocab-1 have no row and are ignored
+ *   workspace  ra_embedding_backward_workspace bytes
+ */
+int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dtype,
+                          const void* ids, int id_dtype, float scale, void* const* dtables, int p,
+                          int64_t vocab, int dtable_dtype, int accumulate, void* workspace,
+                          int64_t workspace_bytes, hipStream_t stream);
+int ra_embedding_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "ra.h")
 RA_OK, RA_ERR_INVALID_ARG, RA_ERR_UNSUPPORTED, RA_ERR_ALIAS = 0, 1, 2, 3
 RA_ERR_MISALIGNED, RA_ERR_HIP, RA_ERR_TIMEOUT = 4, 5, 6
 RA_INT32, RA_FLOAT32, RA_BFLOAT16, RA_FLOAT16, RA_FLOAT64, RA_INT64 = 0, 1, 2, 3, 4, 5
+RA_FLOAT8_E4M3 = 6
 RA_SUM, RA_MAX, RA_AVG = 0, 1, 2
 RA_MAX_RANKS = 64
 RA_FLAG_FORCE_TIMEOUT = 1
@@ -61,6 +62,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 _SIGNATURES = {
     "ra_chunk_bounds": (_int, [_i64, _int, ctypes.POINTER(ctypes.c_int64)]),
@@ -83,6 +85,20 @@ _SIGNATURES = {
     "ra_wallclock_hz": (_int, [ctypes.POINTER(ctypes.c_int64)]),
     "ra_stream_copy": (_int, [_vp, _vp, _i64, _vp]),
     "ra_stream_copy_resident": (_int, [_vp, _vp, _i64, _int, _vp]),
+    "ra_allreduce_rmsnorm": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _int, _vp, _f32, _vp,
+                                    _int, _int, _vp, _int, _vp, _vp]),
+    "ra_allreduce_rmsnorm_backward": (_int, [_vp, _int, _i64, _i64, _int, _vp, _int, _vp, _vp, _vp,
+                                             _vp, _vp, _int, _vp, _vp, _i64, _vp]),
+    "ra_rmsnorm_backward_workspace": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "ra_cross_entropy": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp,
+                                _f32, _vp, _i64, _vp]),
+    "ra_cross_entropy_workspace": (_int, [_i64, _i64, _int, ctypes.POINTER(_i64)]),
+    "ra_cross_entropy_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _vp, _vp,
+                                         _vp, _f32, _vp]),
+    "ra_embedding": (_int, [_vp, _int, _i64, _i64, _int, _vp, _int, _i64, _f32, _vp, _int, _vp]),
+    "ra_embedding_backward": (_int, [_vp, _i64, _i64, _int, _vp, _int, _f32, _vp, _int, _i64, _int,
+                                     _int, _vp, _i64, _vp]),
+    "ra_embedding_backward_workspace": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
 }
 
 
@@ -317,3 +333,268 @@ def ra_stream_copy_resident(dst, src, grid=0, stream=None):
     return _check(lib().ra_stream_copy_resident(ctypes.c_void_p(dst.data_ptr()),
                                                 ctypes.c_void_p(src.data_ptr()), nbytes,
                                                 int(grid), _stream_handle(stream, src.device)))
+
+
+# ---------------------------------------------------------------- row operators
+# Tensors are [tokens, hidden], or have those as their last dimensions flattened:
+# only the number of elements and the last dimension count.  The calls write into
+# the tensors they are given and return None; scratch memory is taken from torch's
+# allocator on the call's stream, so that a captured graph owns its own.
+
+def _rank_list(what, tensors, like):
+    """Pointer table of a list of tensors that share one dtype and the device of `like`."""
+    ptrs = (ctypes.c_void_p * max(1, len(tensors)))()
+    dt, dev = tensors[0].dtype if len(tensors) else None, like.device
+    for i, t in enumerate(tensors):
+        if t.dtype is not dt or t.device != dev:
+            raise ValueError(f"{what} must share one dtype and the device of the other tensors")
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+        ptrs[i] = t.data_ptr()
+    return ptrs
+
+
+def _arg(what, t, like, numel, dtype=None):
+    """Pointer of one tensor (None: NULL), checked."""
+    if t is None:
+        return None
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on the device of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements, expected {numel}")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _sizes(what, tensors, numel):
+    for t in tensors:
+        if t.numel() != numel:
+            raise ValueError(f"{what} have {t.numel()} elements, expected {numel}")
+
+
+def _tensors(bufs):
+    ts = bufs.tensors if isinstance(bufs, RankBuffers) else bufs
+    if len(ts) == 0:
+        raise ValueError("need at least one rank buffer")
+    if not ts[0].is_cuda:
+        raise ValueError("rank buffers must be device tensors")
+    return ts
+
+
+def _run_on(like, stream, call):
+    """call(stream handle) with the tensors' device current."""
+    torch = _torch()
+    dev = like.get_device()
+    if torch.cuda.current_device() == dev:
+        return _check(call(_stream_handle(stream, dev)))
+    with torch.cuda.device(dev):
+        return _check(call(_stream_handle(stream, dev)))
+
+
+def _scratch(like, stream, size_call, *sizes):
+    """(tensor, bytes) of workspace, allocated for the stream the call runs on."""
+    torch = _torch()
+    n = ctypes.c_int64()
+    _check(size_call(*sizes, ctypes.byref(n)))
+    if n.value == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(n.value, dtype=torch.uint8, device=like.device), n.value
+    with torch.cuda.stream(stream):
+        return torch.empty(n.value, dtype=torch.uint8, device=like.device), n.value
+
+
+def _workspace(workspace, like, stream, size_call, *sizes):
+    """(tensor to keep alive, pointer, bytes): the caller's tensor, or scratch."""
+    if workspace is None:
+        workspace, n = _scratch(like, stream, size_call, *sizes)
+        return workspace, None if workspace is None else workspace.data_ptr(), n
+    n = workspace.numel() * workspace.element_size()
+    return workspace, _arg("workspace", workspace, like, workspace.numel()), n
+
+
+def ra_rmsnorm_backward_workspace(tokens, hidden):
+    """Bytes of workspace (host only)."""
+    n = ctypes.c_int64()
+    _check(lib().ra_rmsnorm_backward_workspace(int(tokens), int(hidden), ctypes.byref(n)))
+    return n.value
+
+
+def ra_cross_entropy_workspace(tokens, vocab, p):
+    """Bytes of workspace (host only)."""
+    n = ctypes.c_int64()
+    _check(lib().ra_cross_entropy_workspace(int(tokens), int(vocab), int(p), ctypes.byref(n)))
+    return n.value
+
+
+def ra_embedding_backward_workspace(tokens, hidden):
+    """Bytes of workspace (host only)."""
+    n = ctypes.c_int64()
+    _check(lib().ra_embedding_backward_workspace(int(tokens), int(hidden), ctypes.byref(n)))
+    return n.value
+
+
+def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=None, scales=None,
+                         group=0, rstd=None, stream=None):
+    """outs = RMS norm of (residual + the sum of bufs) times weight; see include/ra.h.
+
+    bufs, outs: lists of tensors (bufs: or a RankBuffers).  outs of float8_e4m3fn take
+    scales: as many float32 tensors, one value a token or a group of columns."""
+    torch = _torch()
+    ts = _tensors(bufs)
+    ptrs, p, n, dt, _ = _marshal(bufs)
+    b0, hidden = ts[0], weight.numel()
+    if hidden == 0 or n % hidden:
+        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
+    tokens = n // hidden
+    if len(outs) == 0:
+        raise ValueError("need at least one output")
+    f8 = outs[0].dtype is torch.float8_e4m3fn
+    _sizes("outs", outs, n)
+    res = residual if residual is not None else residual_out
+    res_code = dtype_code(res) if res is not None else dt
+    res_type = res.dtype if res is not None else None
+    scale_ptrs = None
+    if f8:
+        if scales is None or len(scales) != len(outs):
+            raise ValueError("8-bit outputs need as many scales")
+        _sizes("scales", scales, tokens * (-(-hidden // group) if group > 0 else 1))
+        if scales[0].dtype is not torch.float32:
+            raise TypeError("scales must be float32")
+        scale_ptrs = _rank_list("scales", scales, b0)
+    args = (ptrs, p, tokens, hidden, dt, _arg("residual", residual, b0, n, res_type),
+            _arg("residual_out", residual_out, b0, n, res_type), res_code,
+            _arg("weight", weight, b0, hidden, b0.dtype), eps, _rank_list("outs", outs, b0),
+            len(outs), RA_FLOAT8_E4M3 if f8 else dtype_code(outs[0]), scale_ptrs, int(group),
+            _arg("rstd", rstd, b0, tokens, torch.float32))
+    _run_on(b0, stream, lambda s: lib().ra_allreduce_rmsnorm(*args, s))
+
+
+def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), dweight=None,
+                                  workspace=None, stream=None):
+    """Gradient of ra_allreduce_rmsnorm from the ranks' parts dys of the gradient of its
+    output; see include/ra.h."""
+    torch = _torch()
+    ts = _tensors(dys)
+    ptrs, p, n, dt, _ = _marshal(dys)
+    d0, hidden = ts[0], weight.numel()
+    if hidden == 0 or n % hidden:
+        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
+    tokens = n // hidden
+    _sizes("dxs", dxs, n)
+    if len(dxs) and dxs[0].dtype is not d0.dtype:
+        raise TypeError(f"dxs must be {d0.dtype}")
+    keep, wp, wn = None, None, 0
+    if dweight is not None:
+        keep, wp, wn = _workspace(workspace, d0, stream, lib().ra_rmsnorm_backward_workspace,
+                                  tokens, hidden)
+    args = (ptrs, p, tokens, hidden, dt, _arg("h", h, d0, n), dtype_code(h),
+            _arg("rstd", rstd, d0, tokens, torch.float32),
+            _arg("weight", weight, d0, hidden, d0.dtype), _arg("dh_in", dh_in, d0, n, h.dtype),
+            _arg("dh", dh, d0, n, h.dtype), _rank_list("dxs", dxs, d0), len(dxs),
+            _arg("dweight", dweight, d0, hidden, torch.float32), wp, wn)
+    _run_on(d0, stream, lambda s: lib().ra_allreduce_rmsnorm_backward(*args, s))
+
+
+def _index_code(what, t):
+    torch = _torch()
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what} must be int32 or int64, not {t.dtype}")
+    return dtype_code(t)
+
+
+def _pieces(what, tensors, dim):
+    """Total length of `dim` over the ranks, checked to be cut as ra_chunk_bounds cuts it."""
+    sizes = [t.shape[dim] for t in tensors]
+    total, p = sum(sizes), len(sizes)
+    base, extra = divmod(total, p)
+    if any(s != base + (r < extra) for r, s in enumerate(sizes)):
+        raise ValueError(f"{what}: {sizes} is not how ra_chunk_bounds cuts {total} over {p} ranks")
+    return total
+
+
+def _logits(logits, targets, grads):
+    ts = _tensors(logits)
+    tokens = targets.numel()
+    if any(t.dim() != 2 or t.shape[0] != tokens for t in ts):
+        raise ValueError("logits must be [tokens, columns of the rank]")
+    vocab = _pieces("logits", ts, 1)
+    if grads is not None:
+        if len(grads) != len(ts) or any(g.shape != t.shape for g, t in zip(grads, ts)):
+            raise ValueError("grads must have the logits' shapes")
+        if grads[0].dtype is not ts[0].dtype:
+            raise TypeError(f"grads must be {ts[0].dtype}")
+    return ts, len(ts), tokens, vocab
+
+
+def ra_cross_entropy(logits, targets, loss=None, lse=None, grads=None, dloss=None, grad_scale=1.0,
+                     valid=None, workspace=None, stream=None):
+    """Softmax cross entropy over a vocabulary cut over the ranks, with its gradient where
+    grads are given (they may be the logits themselves); see include/ra.h.
+
+    logits: a list of [tokens, columns of the rank] tensors."""
+    torch = _torch()
+    ts, p, tokens, vocab = _logits(logits, targets, grads)
+    x0 = ts[0]
+    keep, wp, wn = _workspace(workspace, x0, stream, lib().ra_cross_entropy_workspace,
+                              tokens, vocab, p)
+    args = (_rank_list("logits", ts, x0), p, tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), _arg("targets", targets, x0, tokens), _index_code("targets", targets),
+            _arg("loss", loss, x0, tokens, torch.float32), _arg("lse", lse, x0, tokens, torch.float32),
+            None if grads is None else _rank_list("grads", grads, x0),
+            _arg("dloss", dloss, x0, tokens, torch.float32), grad_scale, wp, wn)
+    _run_on(x0, stream, lambda s: lib().ra_cross_entropy(*args, s))
+
+
+def ra_cross_entropy_backward(logits, targets, lse, grads, dloss=None, grad_scale=1.0, valid=None,
+                              stream=None):
+    """The gradient of ra_cross_entropy from the logits and lse; see include/ra.h."""
+    torch = _torch()
+    ts, p, tokens, vocab = _logits(logits, targets, grads)
+    x0 = ts[0]
+    args = (_rank_list("logits", ts, x0), p, tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), _arg("targets", targets, x0, tokens), _index_code("targets", targets),
+            _arg("lse", lse, x0, tokens, torch.float32), _rank_list("grads", grads, x0),
+            _arg("dloss", dloss, x0, tokens, torch.float32), grad_scale)
+    _run_on(x0, stream, lambda s: lib().ra_cross_entropy_backward(*args, s))
+
+
+def _tables(what, tables):
+    ts = _tensors(tables)
+    hidden = ts[0].shape[-1] if ts[0].dim() == 2 else 0
+    if any(t.dim() != 2 or t.shape[1] != hidden for t in ts):
+        raise ValueError(f"{what} must be [rows of the rank, hidden]")
+    return ts, len(ts), _pieces(what, ts, 0), hidden
+
+
+def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
+    """outs = scale times the rows of a table cut over the ranks; see include/ra.h.
+
+    tables: a list of [rows of the rank, hidden] tensors."""
+    ts, p, vocab, hidden = _tables("tables", tables)
+    t0, tokens = ts[0], ids.numel()
+    if len(outs) == 0:
+        raise ValueError("need at least one output")
+    _sizes("outs", outs, tokens * hidden)
+    if outs[0].dtype is not t0.dtype:
+        raise TypeError(f"outs must be {t0.dtype}")
+    args = (_rank_list("tables", ts, t0), p, vocab, hidden, dtype_code(t0),
+            _arg("ids", ids, t0, tokens), _index_code("ids", ids), tokens, scale,
+            _rank_list("outs", outs, t0), len(outs))
+    _run_on(t0, stream, lambda s: lib().ra_embedding(*args, s))
+
+
+def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspace=None, stream=None):
+    """dtables = (or with accumulate +=) scale times the sums of dy's rows by token; see
+    include/ra.h."""
+    ts, p, vocab, hidden = _tables("dtables", dtables)
+    t0, tokens = ts[0], ids.numel()
+    keep, wp, wn = _workspace(workspace, t0, stream, lib().ra_embedding_backward_workspace,
+                              tokens, hidden)
+    args = (_arg("dy", dy, t0, tokens * hidden), tokens, hidden, dtype_code(dy),
+            _arg("ids", ids, t0, tokens), _index_code("ids", ids), scale,
+            _rank_list("dtables", ts, t0), p, vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
+    _run_on(t0, stream, lambda s: lib().ra_embedding_backward(*args, s))

@@ -21,8 +21,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libra.so")
 
-SOURCES = ["ra_fused.hip", "ra_rider.hip", "ra_steps.hip", "ra_copy.hip", "ra_api.cpp"]
-HEADERS = ["ra_elem.h", "ra_sync.h", "ra_internal.h"]
+SOURCES = ["ra_fused.hip", "ra_rider.hip", "ra_steps.hip", "ra_copy.hip", "ra_norm.hip",
+           "ra_xent.hip", "ra_embed.hip", "ra_rows_api.cpp", "ra_api.cpp"]
+HEADERS = ["ra_elem.h", "ra_rows.h", "ra_sync.h", "ra_internal.h"]
 
 
 def hipcc():

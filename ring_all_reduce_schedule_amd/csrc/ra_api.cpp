@@ -21,8 +21,10 @@
 #include "ra_internal.h"
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace ra {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -45,6 +47,14 @@ bool debug_on() {
   }();
   return on != 0;
 }
+
+}  // namespace ra
+
+namespace {
+
+using ra::debug_on;
+using ra::fail;
+using ra::fail_hip;
 
 constexpr int kLastAlgo = RA_ALGO_RING_PIPELINED_FLAGS;
 

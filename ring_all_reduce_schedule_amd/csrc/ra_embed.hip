@@ -1,0 +1,416 @@
+// ra_embed.hip -- rows of an embedding table whose vocabulary is cut over the
+// ranks, and the gradient of those rows.
+//
+//   y_t = scale W[id_t],     dW[v] = scale * sum over {t: id_t = v} of dy_t  (+ dW[v])
+//
+// A rank that does not hold id_t would add a row of zeros to the sum over the
+// ranks; here the one row that counts is read from the rank that holds it and
+// written to every rank.
+//
+// The gradient adds up the rows of equal tokens in the order of their positions,
+// so it does not depend on how the work was scheduled: positions are sorted by
+// token (a stable sort), the sorted positions are cut into stretches of equal
+// length, and each stretch adds up its runs of equal tokens in float32.  A run
+// inside one stretch is written at once; the sums of a run that crosses stretches
+// go to the workspace and are joined afterwards in order.  Cutting by positions
+// and not by tokens keeps the work even: in text the most frequent token makes up
+// several percent of all.  No atomics on floats are used.
+#include "ra_rows.h"
+
+namespace ra {
+namespace {
+
+__device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t t) {
+  return ids64 ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
+}
+
+// G lanes to a token and 256 / G tokens to a workgroup; a token's units go over
+// gridDim.y and the lanes.
+template <int DT, int G, bool AL>
+__global__ __launch_bounds__(256) void k_embed(EmbedArgs a) {
+  const int64_t t = a.row0 + (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  const int j = blockIdx.y * G + threadIdx.x % G;
+  if (t >= a.tokens || j * kU >= a.hidden) return;
+  const Cut u = unit_cut<AL>(j, a.hidden);
+  const int64_t id = load_id(a.ids, a.ids64, t);
+  float y[kU];
+  if (id >= 0 && id < a.vocab) {
+    const int r = piece_of(a.cut, (int)id);
+    const Unit<DT> w = load_cut<DT, AL>(a.table.b[r], (id - piece_lo(a.cut, r)) * a.hidden, u);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) y[i] = unit_get<DT>(w, i) * a.scale;
+  } else {
+    const float none = id < 0 ? 0.0f : __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) y[i] = none;
+  }
+  const Unit<DT> out = unit_make<DT>(y);
+  for (int r = 0; r < a.n_out; ++r) store_cut<DT, AL>(a.out.b[r], t * a.hidden, u, out);
+}
+
+// ---------------------------------------------------------------- sorting positions by token
+
+// Keys: the token, or `vocab` for what has no row, which sorts behind all rows.
+__device__ __forceinline__ int key_of(const EmbedBwdArgs& a, int64_t t) {
+  const int64_t id = load_id(a.ids, a.ids64, t);
+  return id >= 0 && id < a.vocab ? (int)id : a.vocab;
+}
+
+// Few positions: each finds its place by counting the keys before it.
+constexpr int kCountMost = 4096;
+__global__ __launch_bounds__(256) void k_sort_count(EmbedBwdArgs a, int* keys, int* pos) {
+  __shared__ __align__(16) int lds[kCountMost];
+  const int n = (int)a.tokens, up = (n + 3) / 4 * 4;
+  for (int i = threadIdx.x; i < up; i += 256) lds[i] = i < n ? key_of(a, i) : 0x7fffffff;
+  __syncthreads();
+  const int me = blockIdx.x * 256 + threadIdx.x;
+  if (me >= n) return;
+  const int key = lds[me];
+  int at = 0;
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll 4
+  for (int i = 0; i < up; i += 4) {
+    const i32x4 k = *reinterpret_cast<const i32x4*>(lds + i);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) at += k[c] < key || (k[c] == key && i + c < me) ? 1 : 0;
+  }
+  keys[at] = key;
+  pos[at] = me;
+}
+
+// More: passes over digits of kBits bits, lowest first, each a stable counting
+// sort of blocks of kTile keys.
+constexpr int kBits = 9, kBins = 1 << kBits, kSortThreads = 512, kTile = 4096;
+constexpr int kPerLane = kTile / kSortThreads;      // 8
+constexpr int kSortWaves = kSortThreads / 64;
+
+// Key and position number i of a pass's input; the first pass reads the tokens.
+struct SortIn {
+  const int* keys;     // null: the tokens themselves
+  const int* pos;
+};
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_hist(EmbedBwdArgs a, SortIn in, int shift, int* hist) {
+  __shared__ int bins[kBins];
+  for (int i = threadIdx.x; i < kBins; i += kSortThreads) bins[i] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * kTile;
+  for (int k = 0; k < kPerLane; ++k) {
+    const int64_t i = lo + k * kSortThreads + threadIdx.x;
+    if (i < a.tokens) {
+      const int key = in.keys ? in.keys[i] : key_of(a, i);
+      atomicAdd(&bins[(key >> shift) & (kBins - 1)], 1);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kSortThreads) hist[(int64_t)blockIdx.x * kBins + i] = bins[i];
+}
+
+// A block's keys go behind all keys of lower digits, and behind the earlier
+// blocks' keys of the same digit; inside the block wave by wave (a wave has
+// neighbouring keys), inside a wave round by round and lane by lane.
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, SortIn in, int shift,
+                                                             const int* hist, int blocks, int* keys, int* pos) {
+  __shared__ int place[kSortWaves][kBins];   // keys of a digit in a wave, then where they start
+  __shared__ int total[kBins];
+  const int tid = threadIdx.x, w = tid / 64, lane = tid % 64;
+  static_assert(kSortThreads == kBins, "a thread to a digit");
+  // digit tid: how many keys there are, and how many in earlier blocks
+  int before = 0, all = 0;
+  for (int b = 0; b < blocks; ++b) {
+    const int n = hist[(int64_t)b * kBins + tid];
+    before += b < (int)blockIdx.x ? n : 0;
+    all += n;
+  }
+  for (int i = 0; i < kSortWaves; ++i) place[i][tid] = 0;
+  total[tid] = all;
+  __syncthreads();
+  // sum over the lower digits
+  for (int d = 1; d < kBins; d *= 2) {
+    const int add = tid >= d ? total[tid - d] : 0;
+    __syncthreads();
+    total[tid] += add;
+    __syncthreads();
+  }
+  const int64_t lo = (int64_t)blockIdx.x * kTile + w * (kTile / kSortWaves);
+  int key[kPerLane], rank[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    const int64_t i = lo + k * 64 + lane;
+    const bool in_range = i < a.tokens;
+    key[k] = !in_range ? 0 : in.keys ? in.keys[i] : key_of(a, i);
+    const int digit = (key[k] >> shift) & (kBins - 1);
+    uint64_t same = __ballot(in_range);
+#pragma unroll
+    for (int b = 0; b < kBits; ++b) {
+      const bool bit = (digit >> b) & 1;
+      const uint64_t set = __ballot(bit);
+      same &= bit ? set : ~set;
+    }
+    const uint64_t lower = same & ((1ull << lane) - 1);
+    rank[k] = 0;
+    if (in_range) {
+      // the lanes of a digit read its count before the last of them raises it
+      const int at = place[w][digit];
+      rank[k] = at + __popcll(lower);
+      __builtin_amdgcn_wave_barrier();
+      if ((same >> lane) == 1) place[w][digit] = rank[k] + 1;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __syncthreads();
+  int at = (tid > 0 ? total[tid - 1] : 0) + before;
+  for (int i = 0; i < kSortWaves; ++i) {
+    const int n = place[i][tid];
+    place[i][tid] = at;
+    at += n;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    const int64_t i = lo + k * 64 + lane;
+    if (i < a.tokens) {
+      const int to = place[w][(key[k] >> shift) & (kBins - 1)] + rank[k];
+      keys[to] = key[k];
+      pos[to] = in.pos ? in.pos[i] : (int)i;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- adding up the runs
+
+// Sorted positions of one stretch, and rows that one workgroup clears.
+constexpr int kRun = 16, kClear = 8;
+
+struct RunArgs {
+  const int* keys;
+  const int* pos;
+  float* part;       // [stretches][2][hidden]: a stretch's first and last run, where they cross its ends
+  int32_t sorted;    // positions
+  int32_t stretches, clears, columns;   // workgroups: stretches * columns, then clears
+};
+
+template <int TT, bool AL>
+__device__ __forceinline__ void put_row(const EmbedBwdArgs& a, int key, const Cut& u, const float* sum) {
+  const int r = piece_of(a.cut, key);
+  const int64_t row = (int64_t)(key - piece_lo(a.cut, r)) * a.hidden;
+  float y[kU];
+#pragma unroll
+  for (int i = 0; i < kU; ++i) y[i] = sum[i] * a.scale;
+  if (a.accumulate) {
+    const Unit<TT> old = load_cut<TT, AL>(a.table.b[r], row, u);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) y[i] += unit_get<TT>(old, i);
+  }
+  store_cut<TT, AL>(a.table.b[r], row, u, unit_make<TT>(y));
+}
+
+// First sorted place whose key is at least `key`, by the whole wave: each round
+// looks at 64 places.
+__device__ __forceinline__ int lower_bound(const int* keys, int n, int key) {
+  int lo = 0, hi = n;                  // the answer is in [lo, hi]
+  const int lane = threadIdx.x % 64;
+  while (hi > lo) {
+    const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const bool less = at < hi && keys[at] < key;
+    const int below = __popcll(__ballot(less));      // keys ascend: the first lanes
+    if (below == 0) return lo;
+    const int from = lo + (below - 1) * step + 1;
+    hi = min(hi, lo + below * step);
+    lo = from;
+  }
+  return lo;
+}
+
+template <int DT, int TT, bool AL>
+__global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
+  if ((int)blockIdx.x >= g.stretches * g.columns) {
+    // rows no token has: zeros
+    __shared__ int taken[kClear];
+    const int v0 = ((int)blockIdx.x - g.stretches * g.columns) * kClear;
+    const int v1 = min(a.vocab, v0 + kClear);
+    if (threadIdx.x < kClear) taken[threadIdx.x] = 0;
+    __syncthreads();
+    const int from = lower_bound(g.keys, g.sorted, v0), to = lower_bound(g.keys, g.sorted, v1);
+    for (int i = from + (int)threadIdx.x; i < to; i += 256) taken[g.keys[i] - v0] = 1;
+    __syncthreads();
+    const Unit<TT> zero{};
+    for (int v = v0; v < v1; ++v) {
+      if (taken[v - v0]) continue;
+      const int r = piece_of(a.cut, v);
+      const int64_t row = (int64_t)(v - piece_lo(a.cut, r)) * a.hidden;
+      for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
+        store_cut<TT, AL>(a.table.b[r], row, unit_cut<AL>(j, a.hidden), zero);
+    }
+    return;
+  }
+  const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
+  const int lo = stretch * kRun, hi = min(g.sorted, lo + kRun);
+  if (j * kU >= a.hidden) return;
+  const Cut u = unit_cut<AL>(j, a.hidden);
+  // all the stretch's rows at once
+  Unit<DT> rows[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k)
+    if (lo + k < hi) rows[k] = load_cut<DT, AL>(a.dy, (int64_t)g.pos[lo + k] * a.hidden, u);
+  const int before = lo > 0 ? g.keys[lo - 1] : -1, after = hi < g.sorted ? g.keys[hi] : -1;
+  float sum[kU];
+#pragma unroll
+  for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
+  int start = lo;
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    if (lo + k < hi) {
+      const int key = g.keys[lo + k];
+      if (key < a.vocab) {
+        unit_add<DT>(sum, rows[k]);
+        const bool last = lo + k + 1 == hi;
+        if (last || g.keys[lo + k + 1] != key) {
+          const bool open_before = start == lo && before == key, open_after = last && after == key;
+          if (open_before || open_after) {
+            const int64_t slot = ((int64_t)stretch * 2 + (open_before ? 0 : 1)) * a.hidden;
+            store_cut<1, AL>(g.part, slot, u, unit_make<1>(sum));
+          } else {
+            put_row<TT, AL>(a, key, u, sum);
+          }
+          start = lo + k + 1;
+#pragma unroll
+          for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
+        }
+      }
+    }
+  }
+}
+
+// Runs that cross stretches: the stretch a run begins in adds up its parts, its
+// own first, then the following stretches' first parts.
+template <int TT, bool AL>
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g) {
+  const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
+  const int lo = stretch * kRun, hi = lo + kRun;
+  if (hi >= g.sorted) return;                       // the last stretch: nothing follows
+  const int key = g.keys[hi - 1];
+  if (key >= a.vocab || g.keys[hi] != key) return;
+  // it began before this stretch, which all belongs to it
+  if (lo > 0 && g.keys[lo] == key && g.keys[lo - 1] == key) return;
+  // where it ends: the place after its last position (the whole wave searches)
+  const int end = lower_bound(g.keys, g.sorted, key + 1);
+  const int last = (end - 1) / kRun;                // the stretch of that position
+  if (j * kU >= a.hidden) return;
+  const Cut u = unit_cut<AL>(j, a.hidden);
+  float sum[kU];
+#pragma unroll
+  for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
+  unit_add<1>(sum, load_cut<1, AL>(g.part, ((int64_t)stretch * 2 + 1) * a.hidden, u));
+#pragma unroll 8
+  for (int s = stretch + 1; s <= last; ++s)
+    unit_add<1>(sum, load_cut<1, AL>(g.part, (int64_t)s * 2 * a.hidden, u));
+  put_row<TT, AL>(a, key, u, sum);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launches
+
+template <int DT, int G>
+static hipError_t embed_go(const EmbedArgs& args, bool al, hipStream_t s) {
+  constexpr int64_t kMost = 1ll << 20;      // x blocks; with y the dispatch counts 32 bits of threads
+  EmbedArgs a = args;
+  const int units = (a.hidden + kU - 1) / kU, cols = (units + G - 1) / G;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMost, 0xFFFFFFFFll / 256 / cols));
+  for (; a.row0 < a.tokens; a.row0 += most * (256 / G)) {
+    const dim3 grid((unsigned)std::min<int64_t>(most, (a.tokens - a.row0 + 256 / G - 1) / (256 / G)), cols);
+    if (al) k_embed<DT, G, true><<<grid, 256, 0, s>>>(a);
+    else k_embed<DT, G, false><<<grid, 256, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT>
+static hipError_t embed_size(const EmbedArgs& a, bool al, hipStream_t s) {
+  const int units = (a.hidden + kU - 1) / kU;
+  return units <= 64 ? embed_go<DT, 64>(a, al, s) : embed_go<DT, 256>(a, al, s);
+}
+
+hipError_t launch_embed(const EmbedArgs& a, int dtype, bool al, hipStream_t s) {
+  if (dtype == 1) return embed_size<1>(a, al, s);
+  if (dtype == 2) return embed_size<2>(a, al, s);
+  return embed_size<3>(a, al, s);
+}
+
+// The workspace: sorted keys and positions (twice where the sort takes passes),
+// the passes' counts, the open runs' sums.  Each part starts on 16 bytes.
+static int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
+static int sort_blocks(int64_t tokens) { return tokens <= kCountMost ? 0 : (int)((tokens + kTile - 1) / kTile); }
+static int64_t stretches_of(int64_t tokens) { return (tokens + kRun - 1) / kRun; }
+
+int64_t embed_bwd_words(int64_t tokens, int hidden) {
+  const int64_t blocks = sort_blocks(tokens);
+  return (blocks ? 4 : 2) * up4(tokens) + blocks * kBins + stretches_of(tokens) * 2 * hidden;
+}
+
+static int columns_of(int hidden) { return (hidden + 256 * kU - 1) / (256 * kU); }
+
+// One dispatch counts threads in 32 bits.
+bool embed_bwd_fits(int64_t tokens, int vocab, int hidden) {
+  return tokens < (1ll << 31) - kTile &&
+         stretches_of(tokens) * columns_of(hidden) + (vocab + kClear - 1) / kClear <= 0xFFFFFFFFll / 256;
+}
+
+template <int DT, int TT>
+static hipError_t runs_go(const EmbedBwdArgs& a, const RunArgs& g, bool al, hipStream_t s) {
+  const unsigned grid = (unsigned)(g.stretches * g.columns + g.clears);
+  if (grid == 0) return hipSuccess;
+  if (al) k_embed_runs<DT, TT, true><<<grid, 256, 0, s>>>(a, g);
+  else k_embed_runs<DT, TT, false><<<grid, 256, 0, s>>>(a, g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.stretches < 2) return e;
+  const unsigned join = (unsigned)((g.stretches - 1) * g.columns);
+  if (al) k_embed_join<TT, true><<<join, 256, 0, s>>>(a, g);
+  else k_embed_join<TT, false><<<join, 256, 0, s>>>(a, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, bool al, hipStream_t s) {
+  const int64_t n = a.tokens, blocks = sort_blocks(n);
+  int* keys = a.work;
+  int* pos = keys + up4(n);
+  int* spare_keys = pos + up4(n);
+  int* spare_pos = spare_keys + up4(n);
+  int* hist = spare_pos + up4(n);
+  RunArgs g;
+  g.part = reinterpret_cast<float*>(blocks ? hist + blocks * kBins : spare_keys);
+  if (n > 0 && blocks == 0) {
+    k_sort_count<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, keys, pos);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else if (n > 0) {
+    int bits = 1;
+    while ((a.vocab >> bits) != 0) ++bits;          // keys are 0 .. vocab
+    SortIn in = {nullptr, nullptr};
+    for (int shift = 0; shift < bits; shift += kBits) {
+      k_sort_hist<<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist);
+      k_sort_place<<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist, (int)blocks, keys, pos);
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      in = {keys, pos};
+      std::swap(keys, spare_keys);
+      std::swap(pos, spare_pos);
+    }
+    keys = const_cast<int*>(in.keys);
+    pos = const_cast<int*>(in.pos);
+  }
+  g.keys = keys;
+  g.pos = pos;
+  g.sorted = (int32_t)n;
+  g.stretches = (int32_t)stretches_of(n);
+  g.columns = columns_of(a.hidden);
+  g.clears = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
+  if (dtype == 1) return runs_go<1, 1>(a, g, al, s);
+  if (dtype == 2) return table_dtype == 1 ? runs_go<2, 1>(a, g, al, s) : runs_go<2, 2>(a, g, al, s);
+  return table_dtype == 1 ? runs_go<3, 1>(a, g, al, s) : runs_go<3, 3>(a, g, al, s);
+}
+
+}  // namespace ra

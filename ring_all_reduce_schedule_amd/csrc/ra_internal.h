@@ -98,6 +98,111 @@ hipError_t launch_copy_resident(void* dst, const void* src, int64_t bytes, int g
 // Workgroups a persistent step kernel runs by default on the current device.
 int default_persistent_workgroups();
 
+// ---------------------------------------------------------------- row operators
+// What a tensor-parallel model does where it folds its ranks' buffers.  `al`:
+// every row of every array starts on a 16-byte boundary (and its length is a
+// multiple of 8).
+
+struct NormArgs {
+  RankPtrs in, out, scale;   // scale: used by 8-bit outputs
+  const void* res;           // or null
+  void* res_out;             // or null
+  const void* weight;
+  float* rstd;               // or null
+  int64_t tokens, row0;
+  int32_t hidden, p, n_out, group;
+  float eps, inv_h;
+};
+
+struct NormBwdArgs {
+  RankPtrs in, dx;
+  const void* h;
+  const float* rstd;
+  const void* weight;
+  const void* dh_in;         // or null
+  void* dh;
+  float* part;               // [norm_bwd_blocks()][hidden]: the workgroups' sums for dw, or null
+  int64_t tokens;
+  int32_t hidden, p, n_dx;
+  float inv_h;
+};
+
+// Rows longer than this would not stay in the registers of one workgroup.
+constexpr int kNormMaxHidden = 32768;
+
+// Workgroups of the backward pass: two of 1024 threads for each compute unit.  A
+// constant, so that the order in which dw is summed does not depend on the GPU.
+constexpr int kNormBwdBlocks = 512;
+
+hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, bool al, hipStream_t s);
+int norm_bwd_blocks(int64_t tokens);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int h_dtype, float* dweight, bool al, hipStream_t s);
+
+// How a length (a vocabulary) is cut over the ranks.
+struct Pieces {
+  int32_t base;    // floor(n / p)
+  int32_t extra;   // n mod p: the first `extra` pieces hold one more
+};
+
+struct XentArgs {
+  RankPtrs x, dx;            // the ranks' logits; their gradients (dx.b[0..p) null: not wanted)
+  const void* target;
+  const float* dloss;        // or null: 1 for every token
+  const float* lse_in;       // backward only
+  float* loss;
+  float* lse;
+  float* part;               // split rows: [tokens][splits][2]
+  int64_t tokens, row0;
+  Pieces cut;
+  int32_t p, vocab, valid, target64, splits;
+  int32_t chunks;            // xent_chunks(): chunks of 512 columns to a piece, the last one short
+  uint32_t magic;            // ceil(2^32 / chunks): q / chunks = (q magic) >> 32 while q chunks < 2^32
+  float grad_scale;
+};
+
+// Workgroups that share a row, 1 where a workgroup takes a whole row.
+int xent_splits(int64_t tokens, int vocab, int p);
+int xent_chunks(int vocab, int p);
+
+// Columns of a vocabulary: chunk numbers times chunks stay below 2^32.
+constexpr int kXentMaxVocab = 1 << 24;
+hipError_t launch_xent(const XentArgs& a, int dtype, bool grad, bool al, hipStream_t s);
+hipError_t launch_xent_bwd(const XentArgs& a, int dtype, bool al, hipStream_t s);
+
+struct EmbedArgs {
+  RankPtrs table, out;
+  const void* ids;
+  int64_t tokens;
+  Pieces cut;
+  int64_t row0;
+  int32_t p, vocab, hidden, n_out, ids64;
+  float scale;
+};
+hipError_t launch_embed(const EmbedArgs& a, int dtype, bool al, hipStream_t s);
+
+struct EmbedBwdArgs {
+  RankPtrs table;            // the ranks' gradients
+  const void* dy;
+  const void* ids;
+  int32_t* work;             // see embed_bwd_words
+  int64_t tokens;
+  Pieces cut;
+  int32_t p, vocab, hidden, ids64, accumulate;
+  float scale;
+};
+int64_t embed_bwd_words(int64_t tokens, int hidden);   // 32-bit words of workspace
+bool embed_bwd_fits(int64_t tokens, int vocab, int hidden);
+
+// Elements of an embedding's row (columns of workgroups in one dispatch).
+constexpr int kEmbedMaxHidden = 1 << 20;
+hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, bool al, hipStream_t s);
+
+// ---------------------------------------------------------------- errors
+// Sets the calling thread's error message and returns `code` (ra_api.cpp).
+int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+int fail_hip(hipError_t e, const char* what);
+bool debug_on();
+
 // ---------------------------------------------------------------- host helpers
 
 inline int elem_bytes(int dtype) {
