@@ -93,7 +93,7 @@ XENT_REFUSED = [
     (dict(target_dtype=F32), INV), (dict(logits=None), INV), (dict(logits=[at(0), 0]), INV), (dict(targets=None), INV),
     (dict(grads=[at(5), 0]), INV), (dict(logits=[at(0), at(1) + 1]), MIS), (dict(targets=at(2) + 4), MIS),
     (dict(grads=[at(1), at(0)]), ALI), (dict(grads=[at(0) + 16, at(6)]), ALI), (dict(grads=[at(5), at(5)]), ALI),
-    (dict(lse=at(0)), ALI), (dict(dloss=at(5)), ALI),
+    (dict(dloss=at(5)), ALI),
 ]
 
 
@@ -103,6 +103,7 @@ SPLIT = dict(tokens=8, vocab=32768, valid=32768)
 
 @pytest.mark.parametrize("change,code", XENT_REFUSED + [
     (dict(loss=None, lse=None, grads=None), INV), (dict(loss=at(2)), ALI), (dict(loss=at(4)), ALI),
+    (dict(lse=at(0)), ALI),
     (dict(SPLIT, ws=None), INV), (dict(SPLIT, ws_bytes=100), INV), (dict(SPLIT, ws=at(8) + 8), MIS),
     (dict(SPLIT, ws=at(5)), ALI),
 ])
@@ -114,7 +115,8 @@ XENT_BWD = {k: XENT[k] for k in ("logits", "p", "tokens", "vocab", "valid", "dty
                                  "grads", "dloss", "scale", "stream")}
 
 
-@pytest.mark.parametrize("change,code", XENT_REFUSED + [(dict(grads=None), INV), (dict(lse=None), INV)])
+@pytest.mark.parametrize("change,code", XENT_REFUSED + [(dict(grads=None), INV), (dict(lse=None), INV),
+                                                         (dict(lse=at(5)), ALI)])
 def test_cross_entropy_backward_refusals(change, code):
     assert call("ra_cross_entropy_backward", XENT_BWD, **change) == code
 
