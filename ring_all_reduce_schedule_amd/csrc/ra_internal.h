@@ -151,18 +151,22 @@ struct XentArgs {
   const float* lse_in;       // backward only
   float* loss;
   float* lse;
-  float* part;               // split rows: [tokens][splits][2]
+  float* part;               // split rows: xent_words() of workspace
   int64_t tokens, row0;
   Pieces cut;
   int32_t p, vocab, valid, target64, splits;
-  int32_t chunks;            // xent_chunks(): chunks of 512 columns to a piece, the last one short
-  uint32_t magic;            // ceil(2^32 / chunks): q / chunks = (q magic) >> 32 while q chunks < 2^32
+  // set by xent_geometry() from cut, p, vocab and valid:
+  int32_t whole;             // chunks of 512 columns in a piece
+  int32_t total;             // chunks of a row: those, and what is left of each piece
+  int32_t full;              // the first chunks, all of whose columns are valid
+  uint32_t magic;            // ceil(2^32 / whole): q / whole = (q magic) >> 32 while q whole < 2^32
   float grad_scale;
 };
 
 // Workgroups that share a row, 1 where a workgroup takes a whole row.
 int xent_splits(int64_t tokens, int vocab, int p);
-int xent_chunks(int vocab, int p);
+void xent_geometry(XentArgs* a);
+int64_t xent_words(int64_t tokens, int splits);   // 32-bit words of workspace
 
 // Columns of a vocabulary: chunk numbers times chunks stay below 2^32.
 constexpr int kXentMaxVocab = 1 << 24;

@@ -113,11 +113,11 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
     }
     if constexpr (F8) {
       if (a.group) {
-        // a group is group / 8 neighbouring lanes; lanes past the row hold 0
-        for (int d = a.group / kU / 2; d > 0; d >>= 1) {
-          const uint32_t y = __shfl_xor(here, d);
-          here = here > y ? here : y;
-        }
+        // a group is 4, 8 or 16 neighbouring lanes; lanes past the row hold 0
+        here = max_u32(here, dpp<kDppNeighbour>(here));
+        here = max_u32(here, dpp<kDppPair>(here));
+        if (a.group > 32) here = max_u32(here, dpp<kDppFour>(here));
+        if (a.group > 64) here = max_u32(here, dpp<kDppEight>(here));
         const float amax = f8_amax(here), inv = kF8Max / amax;
         if (in) {
 #pragma unroll

@@ -188,18 +188,61 @@ __device__ __forceinline__ void fold_ranks(float* x, const RankPtrs& P, int p, i
 
 // ---------------------------------------------------------------- reductions
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+// x from another lane of the same 16, by the lane pattern CTRL.  Four patterns in a
+// row give every lane what all 16 have: neighbours, pairs, fours (mirrored in 8),
+// eights (mirrored in 16).  They take an instruction each; a shuffle through LDS
+// takes a round trip.
+constexpr int kDppNeighbour = 0xB1, kDppPair = 0x4E, kDppFour = 0x141, kDppEight = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) { return __uint_as_float(dpp<CTRL>(__float_as_uint(x))); }
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+}
+
+// Over 16 neighbouring lanes, the same in all of them.
+__device__ __forceinline__ float row_sum(float x) {
+  x += dpp<kDppNeighbour>(x);
+  x += dpp<kDppPair>(x);
+  x += dpp<kDppFour>(x);
+  x += dpp<kDppEight>(x);
   return x;
 }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t y = __shfl_xor(x, d);
-    x = x > y ? x : y;
-  }
+__device__ __forceinline__ float row_max(float x) {
+  x = __builtin_fmaxf(x, dpp<kDppNeighbour>(x));
+  x = __builtin_fmaxf(x, dpp<kDppPair>(x));
+  x = __builtin_fmaxf(x, dpp<kDppFour>(x));
+  x = __builtin_fmaxf(x, dpp<kDppEight>(x));
   return x;
+}
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t x) {
+  x = max_u32(x, dpp<kDppNeighbour>(x));
+  x = max_u32(x, dpp<kDppPair>(x));
+  x = max_u32(x, dpp<kDppFour>(x));
+  x = max_u32(x, dpp<kDppEight>(x));
+  return x;
+}
+
+// Over the wave, the same in every lane.  The whole wave has to be active.
+__device__ __forceinline__ float wave_sum(float x) {
+  x = row_sum(x);
+  return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = row_max(x);
+  return __builtin_fmaxf(__builtin_fmaxf(lane_value(x, 0), lane_value(x, 16)),
+                         __builtin_fmaxf(lane_value(x, 32), lane_value(x, 48)));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
+  x = row_max_u32(x);
+  const uint32_t a = __builtin_amdgcn_readlane(x, 0), b = __builtin_amdgcn_readlane(x, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(x, 32), d = __builtin_amdgcn_readlane(x, 48);
+  return max_u32(max_u32(a, b), max_u32(c, d));
 }
 
 // Sum over the WAVES waves of a workgroup, the same in every lane.  `lds` holds

@@ -151,8 +151,7 @@ int64_t norm_bwd_bytes(int64_t tokens, int64_t hidden) {
 }
 
 int64_t xent_bytes(int64_t tokens, int64_t vocab, int p) {
-  const int splits = ra::xent_splits(tokens, (int)vocab, p);
-  return splits > 1 ? tokens * splits * 2 * (int64_t)sizeof(float) : 0;
+  return ra::xent_words(tokens, ra::xent_splits(tokens, (int)vocab, p)) * (int64_t)sizeof(float);
 }
 
 // Logits and gradients of a cross entropy, and what both directions need of them.
@@ -177,8 +176,7 @@ int add_xent(Arrays* to, ra::XentArgs* a, void* const* logits, void* const* grad
   a->target64 = target_dtype == RA_INT64;
   a->dloss = dloss;
   a->grad_scale = grad_scale;
-  a->chunks = ra::xent_chunks((int)vocab, p);
-  a->magic = (uint32_t)(((1ull << 32) + a->chunks - 1) / a->chunks);
+  ra::xent_geometry(a);
   int rc = RA_OK;
   for (int r = 0; r < p && rc == RA_OK; ++r) {
     const int64_t bytes = a->tokens * (a->cut.base + (r < a->cut.extra)) * e;
@@ -386,7 +384,7 @@ int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_
   if (rc != RA_OK) return rc;
   a.lse_in = lse;
   // A row is cut so that a wave has about four chunks.
-  a.splits = (int32_t)std::max<int64_t>(1, (int64_t)a.chunks * p / 16);
+  a.splits = (int32_t)std::max<int64_t>(1, (int64_t)a.total / 16);
   const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
   debug_rows("cross_entropy_backward", p, tokens, vocab, dtype, al, a.splits);
   return launched(ra::launch_xent_bwd(a, dtype, al, stream));
