@@ -341,79 +341,90 @@ def ra_stream_copy_resident(dst, src, grid=0, stream=None):
 # the tensors they are given and return None; scratch memory is taken from torch's
 # allocator on the call's stream, so that a captured graph owns its own.
 
-def _rank_list(what, tensors, like):
-    """Pointer table of a list of tensors that share one dtype and the device of `like`."""
-    ptrs = (ctypes.c_void_p * max(1, len(tensors)))()
-    dt, dev = tensors[0].dtype if len(tensors) else None, like.device
-    for i, t in enumerate(tensors):
-        if t.dtype is not dt or t.device != dev:
-            raise ValueError(f"{what} must share one dtype and the device of the other tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-        ptrs[i] = t.data_ptr()
-    return ptrs
-
-
-def _arg(what, t, like, numel, dtype=None):
-    """Pointer of one tensor (None: NULL), checked."""
-    if t is None:
-        return None
-    if t.device != like.device:
+def _refuse(what, t, numel, dtype, dev):
+    if t.get_device() != dev:
         raise ValueError(f"{what} must be on the device of the other tensors")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{what} has {t.numel()} elements, expected {numel}")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{what} must be contiguous")
+
+
+# Small calls take less time on the GPU than these checks do on the host, so the
+# helpers below make one pass over their tensors and look up nothing twice.
+
+def _table(what, tensors, numel, dtype, dev):
+    """array.array of the tensors' addresses, each checked."""
+    for t in tensors:
+        if (t.dtype is not dtype or t.numel() != numel or t.get_device() != dev
+                or not t.is_contiguous()):
+            _refuse(what, t, numel, dtype, dev)
+    return array.array("Q", [t.data_ptr() for t in tensors])
+
+
+def _tables_of(what, tensors, numels, dtype, dev):
+    """The same for tensors of different lengths."""
+    for t, n in zip(tensors, numels):
+        if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+            _refuse(what, t, n, dtype, dev)
+    return array.array("Q", [t.data_ptr() for t in tensors])
+
+
+def _address(table):
+    """Where a pointer table starts; the caller keeps the table while the call reads it."""
+    return table.buffer_info()[0] if table else None
+
+
+def _arg(what, t, numel, dtype, dev):
+    """Address of one tensor (None: NULL), checked."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        _refuse(what, t, numel, dtype, dev)
     return t.data_ptr()
 
 
-def _sizes(what, tensors, numel):
-    for t in tensors:
-        if t.numel() != numel:
-            raise ValueError(f"{what} have {t.numel()} elements, expected {numel}")
+def _first(what, tensors):
+    if len(tensors) == 0:
+        raise ValueError(f"need at least one tensor in {what}")
+    t = tensors[0]
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be device tensors")
+    return t
 
 
-def _tensors(bufs):
-    ts = bufs.tensors if isinstance(bufs, RankBuffers) else bufs
-    if len(ts) == 0:
-        raise ValueError("need at least one rank buffer")
-    if not ts[0].is_cuda:
-        raise ValueError("rank buffers must be device tensors")
-    return ts
-
-
-def _run_on(like, stream, call):
-    """call(stream handle) with the tensors' device current."""
+def _run_on(dev, stream, function, args):
+    """function(*args, stream handle) with the tensors' device current."""
     torch = _torch()
-    dev = like.get_device()
-    if torch.cuda.current_device() == dev:
-        return _check(call(_stream_handle(stream, dev)))
-    with torch.cuda.device(dev):
-        return _check(call(_stream_handle(stream, dev)))
-
-
-def _scratch(like, stream, size_call, *sizes):
-    """(tensor, bytes) of workspace, allocated for the stream the call runs on."""
-    torch = _torch()
-    n = ctypes.c_int64()
-    _check(size_call(*sizes, ctypes.byref(n)))
-    if n.value == 0:
-        return None, 0
     if stream is None:
-        return torch.empty(n.value, dtype=torch.uint8, device=like.device), n.value
-    with torch.cuda.stream(stream):
-        return torch.empty(n.value, dtype=torch.uint8, device=like.device), n.value
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        return _check(function(*args, handle))
+    with torch.cuda.device(dev):
+        return _check(function(*args, handle))
 
 
 def _workspace(workspace, like, stream, size_call, *sizes):
-    """(tensor to keep alive, pointer, bytes): the caller's tensor, or scratch."""
-    if workspace is None:
-        workspace, n = _scratch(like, stream, size_call, *sizes)
-        return workspace, None if workspace is None else workspace.data_ptr(), n
-    n = workspace.numel() * workspace.element_size()
-    return workspace, _arg("workspace", workspace, like, workspace.numel()), n
+    """(tensor to keep alive, address, bytes): the caller's tensor, or one allocated for the
+    stream that the call runs on."""
+    torch = _torch()
+    if workspace is not None:
+        if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the device of the other tensors")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    n = ctypes.c_int64()
+    _check(size_call(*sizes, ctypes.byref(n)))
+    if n.value == 0:
+        return None, None, 0
+    if stream is None:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=like.device)
+    else:
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=like.device)
+    return workspace, workspace.data_ptr(), n.value
 
 
 def ra_rmsnorm_backward_workspace(tokens, hidden):
@@ -437,6 +448,23 @@ def ra_embedding_backward_workspace(tokens, hidden):
     return n.value
 
 
+def _rows(bufs, weight):
+    """(first tensor, pointer table, address, p, dtype code, tokens, hidden, device index)."""
+    torch = _torch()
+    if isinstance(bufs, RankBuffers):
+        table, p, n, code, _ = _marshal(bufs)
+        b0, at = bufs.tensors[0], table
+    else:
+        b0 = _first("rank buffers", bufs)
+        n, code = b0.numel(), dtype_code(b0)
+        table = _table("rank buffers", bufs, n, b0.dtype, b0.get_device())
+        p, at = len(bufs), _address(table)
+    hidden = weight.numel()
+    if hidden == 0 or n % hidden:
+        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
+    return b0, table, at, p, code, n // hidden, hidden, b0.get_device()
+
+
 def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=None, scales=None,
                          group=0, rstd=None, stream=None):
     """outs = RMS norm of (residual + the sum of bufs) times weight; see include/ra.h.
@@ -444,33 +472,25 @@ def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=No
     bufs, outs: lists of tensors (bufs: or a RankBuffers).  outs of float8_e4m3fn take
     scales: as many float32 tensors, one value a token or a group of columns."""
     torch = _torch()
-    ts = _tensors(bufs)
-    ptrs, p, n, dt, _ = _marshal(bufs)
-    b0, hidden = ts[0], weight.numel()
-    if hidden == 0 or n % hidden:
-        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
-    tokens = n // hidden
-    if len(outs) == 0:
-        raise ValueError("need at least one output")
-    f8 = outs[0].dtype is torch.float8_e4m3fn
-    _sizes("outs", outs, n)
+    b0, table, at, p, code, tokens, hidden, dev = _rows(bufs, weight)
+    n, dtype, f32 = tokens * hidden, b0.dtype, torch.float32
+    out_type = _first("outs", outs).dtype
+    f8 = out_type is torch.float8_e4m3fn
+    out_table = _table("outs", outs, n, out_type, dev)
     res = residual if residual is not None else residual_out
-    res_code = dtype_code(res) if res is not None else dt
-    res_type = res.dtype if res is not None else None
-    scale_ptrs = None
+    res_code, res_type = (code, None) if res is None else (dtype_code(res), res.dtype)
+    scale_table = None
     if f8:
         if scales is None or len(scales) != len(outs):
             raise ValueError("8-bit outputs need as many scales")
-        _sizes("scales", scales, tokens * (-(-hidden // group) if group > 0 else 1))
-        if scales[0].dtype is not torch.float32:
-            raise TypeError("scales must be float32")
-        scale_ptrs = _rank_list("scales", scales, b0)
-    args = (ptrs, p, tokens, hidden, dt, _arg("residual", residual, b0, n, res_type),
-            _arg("residual_out", residual_out, b0, n, res_type), res_code,
-            _arg("weight", weight, b0, hidden, b0.dtype), eps, _rank_list("outs", outs, b0),
-            len(outs), RA_FLOAT8_E4M3 if f8 else dtype_code(outs[0]), scale_ptrs, int(group),
-            _arg("rstd", rstd, b0, tokens, torch.float32))
-    _run_on(b0, stream, lambda s: lib().ra_allreduce_rmsnorm(*args, s))
+        groups = -(-hidden // group) if group > 0 else 1
+        scale_table = _table("scales", scales, tokens * groups, f32, dev)
+    args = (at, p, tokens, hidden, code, _arg("residual", residual, n, res_type, dev),
+            _arg("residual_out", residual_out, n, res_type, dev), res_code,
+            _arg("weight", weight, hidden, dtype, dev), eps, _address(out_table), len(out_table),
+            RA_FLOAT8_E4M3 if f8 else dtype_code(outs[0]), _address(scale_table), int(group),
+            _arg("rstd", rstd, tokens, f32, dev))
+    _run_on(dev, stream, lib().ra_allreduce_rmsnorm, args)
 
 
 def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), dweight=None,
@@ -478,25 +498,18 @@ def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), 
     """Gradient of ra_allreduce_rmsnorm from the ranks' parts dys of the gradient of its
     output; see include/ra.h."""
     torch = _torch()
-    ts = _tensors(dys)
-    ptrs, p, n, dt, _ = _marshal(dys)
-    d0, hidden = ts[0], weight.numel()
-    if hidden == 0 or n % hidden:
-        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
-    tokens = n // hidden
-    _sizes("dxs", dxs, n)
-    if len(dxs) and dxs[0].dtype is not d0.dtype:
-        raise TypeError(f"dxs must be {d0.dtype}")
+    d0, table, at, p, code, tokens, hidden, dev = _rows(dys, weight)
+    n, f32 = tokens * hidden, torch.float32
+    dx_table = _table("dxs", dxs, n, d0.dtype, dev)
     keep, wp, wn = None, None, 0
     if dweight is not None:
         keep, wp, wn = _workspace(workspace, d0, stream, lib().ra_rmsnorm_backward_workspace,
                                   tokens, hidden)
-    args = (ptrs, p, tokens, hidden, dt, _arg("h", h, d0, n), dtype_code(h),
-            _arg("rstd", rstd, d0, tokens, torch.float32),
-            _arg("weight", weight, d0, hidden, d0.dtype), _arg("dh_in", dh_in, d0, n, h.dtype),
-            _arg("dh", dh, d0, n, h.dtype), _rank_list("dxs", dxs, d0), len(dxs),
-            _arg("dweight", dweight, d0, hidden, torch.float32), wp, wn)
-    _run_on(d0, stream, lambda s: lib().ra_allreduce_rmsnorm_backward(*args, s))
+    args = (at, p, tokens, hidden, code, _arg("h", h, n, h.dtype, dev), dtype_code(h),
+            _arg("rstd", rstd, tokens, f32, dev), _arg("weight", weight, hidden, d0.dtype, dev),
+            _arg("dh_in", dh_in, n, h.dtype, dev), _arg("dh", dh, n, h.dtype, dev),
+            _address(dx_table), len(dx_table), _arg("dweight", dweight, hidden, f32, dev), wp, wn)
+    _run_on(dev, stream, lib().ra_allreduce_rmsnorm_backward, args)
 
 
 def _index_code(what, t):
@@ -516,18 +529,22 @@ def _pieces(what, tensors, dim):
     return total
 
 
-def _logits(logits, targets, grads):
-    ts = _tensors(logits)
-    tokens = targets.numel()
-    if any(t.dim() != 2 or t.shape[0] != tokens for t in ts):
+def _xent_args(logits, targets, grads):
+    """(first tensor, tables to keep, arguments up to dtype, targets' arguments, grads' address,
+    tokens, vocab, device index)."""
+    x0 = _first("logits", logits)
+    tokens, dev, dtype = targets.numel(), x0.get_device(), x0.dtype
+    if any(t.dim() != 2 or t.shape[0] != tokens for t in logits):
         raise ValueError("logits must be [tokens, columns of the rank]")
-    vocab = _pieces("logits", ts, 1)
+    vocab = _pieces("logits", logits, 1)
+    numels = [t.numel() for t in logits]
+    table, grad_table = _tables_of("logits", logits, numels, dtype, dev), None
     if grads is not None:
-        if len(grads) != len(ts) or any(g.shape != t.shape for g, t in zip(grads, ts)):
+        if len(grads) != len(logits) or any(g.shape != t.shape for g, t in zip(grads, logits)):
             raise ValueError("grads must have the logits' shapes")
-        if grads[0].dtype is not ts[0].dtype:
-            raise TypeError(f"grads must be {ts[0].dtype}")
-    return ts, len(ts), tokens, vocab
+        grad_table = _tables_of("grads", grads, numels, dtype, dev)
+    goal = (_arg("targets", targets, tokens, targets.dtype, dev), _index_code("targets", targets))
+    return x0, (table, grad_table), goal, tokens, vocab, dev
 
 
 def ra_cross_entropy(logits, targets, loss=None, lse=None, grads=None, dloss=None, grad_scale=1.0,
@@ -536,65 +553,61 @@ def ra_cross_entropy(logits, targets, loss=None, lse=None, grads=None, dloss=Non
     grads are given (they may be the logits themselves); see include/ra.h.
 
     logits: a list of [tokens, columns of the rank] tensors."""
-    torch = _torch()
-    ts, p, tokens, vocab = _logits(logits, targets, grads)
-    x0 = ts[0]
+    f32 = _torch().float32
+    x0, (table, grad_table), goal, tokens, vocab, dev = _xent_args(logits, targets, grads)
     keep, wp, wn = _workspace(workspace, x0, stream, lib().ra_cross_entropy_workspace,
-                              tokens, vocab, p)
-    args = (_rank_list("logits", ts, x0), p, tokens, vocab, vocab if valid is None else int(valid),
-            dtype_code(x0), _arg("targets", targets, x0, tokens), _index_code("targets", targets),
-            _arg("loss", loss, x0, tokens, torch.float32), _arg("lse", lse, x0, tokens, torch.float32),
-            None if grads is None else _rank_list("grads", grads, x0),
-            _arg("dloss", dloss, x0, tokens, torch.float32), grad_scale, wp, wn)
-    _run_on(x0, stream, lambda s: lib().ra_cross_entropy(*args, s))
+                              tokens, vocab, len(table))
+    args = (_address(table), len(table), tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), *goal, _arg("loss", loss, tokens, f32, dev),
+            _arg("lse", lse, tokens, f32, dev), _address(grad_table),
+            _arg("dloss", dloss, tokens, f32, dev), grad_scale, wp, wn)
+    _run_on(dev, stream, lib().ra_cross_entropy, args)
 
 
 def ra_cross_entropy_backward(logits, targets, lse, grads, dloss=None, grad_scale=1.0, valid=None,
                               stream=None):
     """The gradient of ra_cross_entropy from the logits and lse; see include/ra.h."""
-    torch = _torch()
-    ts, p, tokens, vocab = _logits(logits, targets, grads)
-    x0 = ts[0]
-    args = (_rank_list("logits", ts, x0), p, tokens, vocab, vocab if valid is None else int(valid),
-            dtype_code(x0), _arg("targets", targets, x0, tokens), _index_code("targets", targets),
-            _arg("lse", lse, x0, tokens, torch.float32), _rank_list("grads", grads, x0),
-            _arg("dloss", dloss, x0, tokens, torch.float32), grad_scale)
-    _run_on(x0, stream, lambda s: lib().ra_cross_entropy_backward(*args, s))
+    f32 = _torch().float32
+    x0, (table, grad_table), goal, tokens, vocab, dev = _xent_args(logits, targets, grads)
+    args = (_address(table), len(table), tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), *goal, _arg("lse", lse, tokens, f32, dev), _address(grad_table),
+            _arg("dloss", dloss, tokens, f32, dev), grad_scale)
+    _run_on(dev, stream, lib().ra_cross_entropy_backward, args)
 
 
-def _tables(what, tables):
-    ts = _tensors(tables)
-    hidden = ts[0].shape[-1] if ts[0].dim() == 2 else 0
-    if any(t.dim() != 2 or t.shape[1] != hidden for t in ts):
+def _cut_table(what, tables):
+    """(first tensor, pointer table, vocab, hidden, device index) of a table's pieces."""
+    t0 = _first(what, tables)
+    hidden = t0.shape[-1] if t0.dim() == 2 else 0
+    if any(t.dim() != 2 or t.shape[1] != hidden for t in tables):
         raise ValueError(f"{what} must be [rows of the rank, hidden]")
-    return ts, len(ts), _pieces(what, ts, 0), hidden
+    dev = t0.get_device()
+    table = _tables_of(what, tables, [t.numel() for t in tables], t0.dtype, dev)
+    return t0, table, _pieces(what, tables, 0), hidden, dev
 
 
 def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
     """outs = scale times the rows of a table cut over the ranks; see include/ra.h.
 
     tables: a list of [rows of the rank, hidden] tensors."""
-    ts, p, vocab, hidden = _tables("tables", tables)
-    t0, tokens = ts[0], ids.numel()
-    if len(outs) == 0:
-        raise ValueError("need at least one output")
-    _sizes("outs", outs, tokens * hidden)
-    if outs[0].dtype is not t0.dtype:
-        raise TypeError(f"outs must be {t0.dtype}")
-    args = (_rank_list("tables", ts, t0), p, vocab, hidden, dtype_code(t0),
-            _arg("ids", ids, t0, tokens), _index_code("ids", ids), tokens, scale,
-            _rank_list("outs", outs, t0), len(outs))
-    _run_on(t0, stream, lambda s: lib().ra_embedding(*args, s))
+    t0, table, vocab, hidden, dev = _cut_table("tables", tables)
+    tokens = ids.numel()
+    _first("outs", outs)
+    out_table = _table("outs", outs, tokens * hidden, t0.dtype, dev)
+    args = (_address(table), len(table), vocab, hidden, dtype_code(t0),
+            _arg("ids", ids, tokens, ids.dtype, dev), _index_code("ids", ids), tokens, scale,
+            _address(out_table), len(out_table))
+    _run_on(dev, stream, lib().ra_embedding, args)
 
 
 def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspace=None, stream=None):
     """dtables = (or with accumulate +=) scale times the sums of dy's rows by token; see
     include/ra.h."""
-    ts, p, vocab, hidden = _tables("dtables", dtables)
-    t0, tokens = ts[0], ids.numel()
+    t0, table, vocab, hidden, dev = _cut_table("dtables", dtables)
+    tokens = ids.numel()
     keep, wp, wn = _workspace(workspace, t0, stream, lib().ra_embedding_backward_workspace,
                               tokens, hidden)
-    args = (_arg("dy", dy, t0, tokens * hidden), tokens, hidden, dtype_code(dy),
-            _arg("ids", ids, t0, tokens), _index_code("ids", ids), scale,
-            _rank_list("dtables", ts, t0), p, vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
-    _run_on(t0, stream, lambda s: lib().ra_embedding_backward(*args, s))
+    args = (_arg("dy", dy, tokens * hidden, dy.dtype, dev), tokens, hidden, dtype_code(dy),
+            _arg("ids", ids, tokens, ids.dtype, dev), _index_code("ids", ids), scale,
+            _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
+    _run_on(dev, stream, lib().ra_embedding_backward, args)

@@ -26,26 +26,37 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int ids64, int64_t t
 
 // G lanes to a token and 256 / G tokens to a workgroup; a token's units go over
 // gridDim.y and the lanes.
-template <int DT, int G, bool AL>
+template <int DT, int G, int AC>
 __global__ __launch_bounds__(256) void k_embed(EmbedArgs a) {
-  const int64_t t = a.row0 + (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  constexpr int U = 4;
+  const int64_t t0 = a.row0 + ((int64_t)blockIdx.x * (256 / G) + threadIdx.x / G) * U;
   const int j = blockIdx.y * G + threadIdx.x % G;
-  if (t >= a.tokens || j * kU >= a.hidden) return;
-  const Cut u = unit_cut<AL>(j, a.hidden);
-  const int64_t id = load_id(a.ids, a.ids64, t);
-  float y[kU];
-  if (id >= 0 && id < a.vocab) {
-    const int r = piece_of(a.cut, (int)id);
-    const Unit<DT> w = load_cut<DT, AL>(a.table.b[r], (id - piece_lo(a.cut, r)) * a.hidden, u);
+  if (t0 >= a.tokens || j * kU >= a.hidden) return;
+  const Cut u = unit_cut<AC>(j, a.hidden);
+  const int n = (int)min((int64_t)U, a.tokens - t0);
+  int64_t id[U];
+  Unit<DT> w[U];
 #pragma unroll
-    for (int i = 0; i < kU; ++i) y[i] = unit_get<DT>(w, i) * a.scale;
-  } else {
-    const float none = id < 0 ? 0.0f : __uint_as_float(0x7fc00000u);
+  for (int k = 0; k < U; ++k) id[k] = load_id(a.ids, a.ids64, min(t0 + k, a.tokens - 1));
 #pragma unroll
-    for (int i = 0; i < kU; ++i) y[i] = none;
+  for (int k = 0; k < U; ++k) {
+    const int64_t i = id[k] >= 0 && id[k] < a.vocab ? id[k] : 0;
+    const int r = piece_of(a.cut, (int)i);
+    w[k] = load_cut<DT, AC != 0>(a.table.b[r], (i - piece_lo(a.cut, r)) * a.hidden, u);
   }
-  const Unit<DT> out = unit_make<DT>(y);
-  for (int r = 0; r < a.n_out; ++r) store_cut<DT, AL>(a.out.b[r], t * a.hidden, u, out);
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    float y[kU];
+    const float none = id[k] < 0 ? 0.0f : __uint_as_float(0x7fc00000u);
+    const bool ok = id[k] >= 0 && id[k] < a.vocab;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) y[i] = ok ? unit_get<DT>(w[k], i) * a.scale : none;
+    w[k] = unit_make<DT>(y);
+  }
+  for (int r = 0; r < a.n_out; ++r)
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (k < n) store_cut<DT, AC>(a.out.b[r], (t0 + k) * a.hidden, u, w[k]);
 }
 
 // ---------------------------------------------------------------- sorting positions by token
@@ -56,26 +67,39 @@ __device__ __forceinline__ int key_of(const EmbedBwdArgs& a, int64_t t) {
   return id >= 0 && id < a.vocab ? (int)id : a.vocab;
 }
 
-// Few positions: each finds its place by counting the keys before it.
-constexpr int kCountMost = 4096;
-__global__ __launch_bounds__(256) void k_sort_count(EmbedBwdArgs a, int* keys, int* pos) {
+// Few positions: each finds its place by counting the keys before it.  A workgroup
+// has all keys in LDS and 64 positions, and each of its 16 waves counts a
+// sixteenth of the keys for all 64.  That is quadratic work, but in one launch:
+// at kCountMost positions it takes about as long as two passes of the other sort.
+constexpr int kCountMost = 4096, kCountThreads = 1024;
+__global__ __launch_bounds__(kCountThreads) void k_sort_count(EmbedBwdArgs a, int* keys, int* pos) {
   __shared__ __align__(16) int lds[kCountMost];
-  const int n = (int)a.tokens, up = (n + 3) / 4 * 4;
-  for (int i = threadIdx.x; i < up; i += 256) lds[i] = i < n ? key_of(a, i) : 0x7fffffff;
+  constexpr int kWaves = kCountThreads / 64, kStep = kWaves * 4;
+  const int n = (int)a.tokens, up = (n + kStep - 1) / kStep * kStep;
+  for (int i = threadIdx.x; i < up; i += kCountThreads) lds[i] = i < n ? key_of(a, i) : 0x7fffffff;
   __syncthreads();
-  const int me = blockIdx.x * 256 + threadIdx.x;
-  if (me >= n) return;
-  const int key = lds[me];
+  const int w = threadIdx.x / 64, lane = threadIdx.x % 64, me = blockIdx.x * 64 + lane;
+  const int key = lds[min(me, n - 1)];
+  const int per = up / kWaves, lo = w * per;
   int at = 0;
   typedef int i32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll 4
-  for (int i = 0; i < up; i += 4) {
+  for (int i = lo; i < lo + per; i += 4) {
     const i32x4 k = *reinterpret_cast<const i32x4*>(lds + i);
+    // keys before mine, or equal ones before me: k < key + (their position < mine)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) at += k[c] < key || (k[c] == key && i + c < me) ? 1 : 0;
+    for (int c = 0; c < 4; ++c) at += k[c] < key + (i + c < me ? 1 : 0) ? 1 : 0;
   }
-  keys[at] = key;
-  pos[at] = me;
+  __syncthreads();
+  lds[threadIdx.x] = at;
+  __syncthreads();
+  if (w == 0 && me < n) {
+    at = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) at += lds[i * 64 + lane];
+    keys[at] = key;
+    pos[at] = me;
+  }
 }
 
 // More: passes over digits of kBits bits, lowest first, each a stable counting
@@ -95,13 +119,15 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_hist(EmbedBwdArgs a, Sort
   for (int i = threadIdx.x; i < kBins; i += kSortThreads) bins[i] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * kTile;
+  int key[kPerLane];
+#pragma unroll
   for (int k = 0; k < kPerLane; ++k) {
-    const int64_t i = lo + k * kSortThreads + threadIdx.x;
-    if (i < a.tokens) {
-      const int key = in.keys ? in.keys[i] : key_of(a, i);
-      atomicAdd(&bins[(key >> shift) & (kBins - 1)], 1);
-    }
+    const int64_t i = min(lo + k * kSortThreads + threadIdx.x, a.tokens - 1);
+    key[k] = in.keys ? in.keys[i] : key_of(a, i);
   }
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k)
+    if (lo + k * kSortThreads + threadIdx.x < a.tokens) atomicAdd(&bins[(key[k] >> shift) & (kBins - 1)], 1);
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kSortThreads) hist[(int64_t)blockIdx.x * kBins + i] = bins[i];
 }
@@ -116,7 +142,16 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64;
   static_assert(kSortThreads == kBins, "a thread to a digit");
   // digit tid: how many keys there are, and how many in earlier blocks
+  const int64_t lo = (int64_t)blockIdx.x * kTile + w * (kTile / kSortWaves);
+  int key[kPerLane], rank[kPerLane], from[kPerLane];
+#pragma unroll
+  for (int k = 0; k < kPerLane; ++k) {
+    const int64_t i = min(lo + k * 64 + lane, a.tokens - 1);
+    key[k] = in.keys ? in.keys[i] : key_of(a, i);
+    from[k] = in.pos ? in.pos[i] : (int)i;
+  }
   int before = 0, all = 0;
+#pragma unroll 8
   for (int b = 0; b < blocks; ++b) {
     const int n = hist[(int64_t)b * kBins + tid];
     before += b < (int)blockIdx.x ? n : 0;
@@ -132,13 +167,9 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
     total[tid] += add;
     __syncthreads();
   }
-  const int64_t lo = (int64_t)blockIdx.x * kTile + w * (kTile / kSortWaves);
-  int key[kPerLane], rank[kPerLane];
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) {
-    const int64_t i = lo + k * 64 + lane;
-    const bool in_range = i < a.tokens;
-    key[k] = !in_range ? 0 : in.keys ? in.keys[i] : key_of(a, i);
+    const bool in_range = lo + k * 64 + lane < a.tokens;
     const int digit = (key[k] >> shift) & (kBins - 1);
     uint64_t same = __ballot(in_range);
 #pragma unroll
@@ -168,11 +199,10 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kPerLane; ++k) {
-    const int64_t i = lo + k * 64 + lane;
-    if (i < a.tokens) {
+    if (lo + k * 64 + lane < a.tokens) {
       const int to = place[w][(key[k] >> shift) & (kBins - 1)] + rank[k];
       keys[to] = key[k];
-      pos[to] = in.pos ? in.pos[i] : (int)i;
+      pos[to] = from[k];
     }
   }
 }
@@ -187,10 +217,10 @@ struct RunArgs {
   const int* pos;
   float* part;       // [stretches][2][hidden]: a stretch's first and last run, where they cross its ends
   int32_t sorted;    // positions
-  int32_t stretches, clears, columns;   // workgroups: stretches * columns, then clears
+  int32_t stretches, clears, columns, per;   // workgroups: stretches * columns and clears
 };
 
-template <int TT, bool AL>
+template <int TT, int AC>
 __device__ __forceinline__ void put_row(const EmbedBwdArgs& a, int key, const Cut& u, const float* sum) {
   const int r = piece_of(a.cut, key);
   const int64_t row = (int64_t)(key - piece_lo(a.cut, r)) * a.hidden;
@@ -198,11 +228,11 @@ __device__ __forceinline__ void put_row(const EmbedBwdArgs& a, int key, const Cu
 #pragma unroll
   for (int i = 0; i < kU; ++i) y[i] = sum[i] * a.scale;
   if (a.accumulate) {
-    const Unit<TT> old = load_cut<TT, AL>(a.table.b[r], row, u);
+    const Unit<TT> old = load_cut<TT, AC>(a.table.b[r], row, u);
 #pragma unroll
     for (int i = 0; i < kU; ++i) y[i] += unit_get<TT>(old, i);
   }
-  store_cut<TT, AL>(a.table.b[r], row, u, unit_make<TT>(y));
+  store_cut<TT, AC>(a.table.b[r], row, u, unit_make<TT>(y));
 }
 
 // First sorted place whose key is at least `key`, by the whole wave: each round
@@ -222,12 +252,16 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int key) {
   return lo;
 }
 
-template <int DT, int TT, bool AL>
+template <int DT, int TT, int AC>
 __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
-  if ((int)blockIdx.x >= g.stretches * g.columns) {
+  // Workgroups that add up runs wait for scattered rows, those that clear rows only
+  // write: one of the former to every g.per of the latter keeps the memory busy.
+  const int runs = g.stretches * g.columns, turn = (int)blockIdx.x / (g.per + 1);
+  const bool run = turn < runs && (int)blockIdx.x % (g.per + 1) == 0;
+  if (!run) {
     // rows no token has: zeros
     __shared__ int taken[kClear];
-    const int v0 = ((int)blockIdx.x - g.stretches * g.columns) * kClear;
+    const int v0 = ((int)blockIdx.x - min(turn + 1, runs)) * kClear;
     const int v1 = min(a.vocab, v0 + kClear);
     if (threadIdx.x < kClear) taken[threadIdx.x] = 0;
     __syncthreads();
@@ -239,20 +273,26 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
       if (taken[v - v0]) continue;
       const int r = piece_of(a.cut, v);
       const int64_t row = (int64_t)(v - piece_lo(a.cut, r)) * a.hidden;
-      for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
-        store_cut<TT, AL>(a.table.b[r], row, unit_cut<AL>(j, a.hidden), zero);
+      if constexpr (AC != 0) {
+        // 16 bytes a lane, next to each other
+        u32x4* at = reinterpret_cast<u32x4*>(static_cast<char*>(a.table.b[r]) + row * ElemSize<TT>::value);
+        for (int j = threadIdx.x; j < a.hidden / (16 / ElemSize<TT>::value); j += 256) at[j] = u32x4{0, 0, 0, 0};
+      } else {
+        for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
+          store_cut<TT, AC>(a.table.b[r], row, unit_cut<AC>(j, a.hidden), zero);
+      }
     }
     return;
   }
-  const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
+  const int stretch = turn / g.columns, j = turn % g.columns * 256 + threadIdx.x;
   const int lo = stretch * kRun, hi = min(g.sorted, lo + kRun);
   if (j * kU >= a.hidden) return;
-  const Cut u = unit_cut<AL>(j, a.hidden);
+  const Cut u = unit_cut<AC>(j, a.hidden);
   // all the stretch's rows at once
   Unit<DT> rows[kRun];
 #pragma unroll
   for (int k = 0; k < kRun; ++k)
-    if (lo + k < hi) rows[k] = load_cut<DT, AL>(a.dy, (int64_t)g.pos[lo + k] * a.hidden, u);
+    if (lo + k < hi) rows[k] = load_cut<DT, AC>(a.dy, (int64_t)g.pos[lo + k] * a.hidden, u);
   const int before = lo > 0 ? g.keys[lo - 1] : -1, after = hi < g.sorted ? g.keys[hi] : -1;
   float sum[kU];
 #pragma unroll
@@ -269,9 +309,9 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
           const bool open_before = start == lo && before == key, open_after = last && after == key;
           if (open_before || open_after) {
             const int64_t slot = ((int64_t)stretch * 2 + (open_before ? 0 : 1)) * a.hidden;
-            store_cut<1, AL>(g.part, slot, u, unit_make<1>(sum));
+            store_cut<1, AC>(g.part, slot, u, unit_make<1>(sum));
           } else {
-            put_row<TT, AL>(a, key, u, sum);
+            put_row<TT, AC>(a, key, u, sum);
           }
           start = lo + k + 1;
 #pragma unroll
@@ -283,29 +323,43 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
 }
 
 // Runs that cross stretches: the stretch a run begins in adds up its parts, its
-// own first, then the following stretches' first parts.
-template <int TT, bool AL>
-__global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g) {
-  const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
+// own first, then the following stretches' first parts.  64 units of the row to a
+// workgroup, four threads to a unit that take every fourth part: the run of a
+// frequent token has many.
+constexpr int kJoinUnits = 64;
+template <int TT, int AC>
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g, int columns) {
+  __shared__ float lds[3][kU][kJoinUnits];
+  const int stretch = blockIdx.x / columns, x = threadIdx.x % kJoinUnits, y = threadIdx.x / kJoinUnits;
+  const int j = blockIdx.x % columns * kJoinUnits + x;
   const int lo = stretch * kRun, hi = lo + kRun;
   if (hi >= g.sorted) return;                       // the last stretch: nothing follows
   const int key = g.keys[hi - 1];
   if (key >= a.vocab || g.keys[hi] != key) return;
   // it began before this stretch, which all belongs to it
   if (lo > 0 && g.keys[lo] == key && g.keys[lo - 1] == key) return;
-  // where it ends: the place after its last position (the whole wave searches)
+  // where it ends: the place after its last position (whole waves search)
   const int end = lower_bound(g.keys, g.sorted, key + 1);
-  const int last = (end - 1) / kRun;                // the stretch of that position
-  if (j * kU >= a.hidden) return;
-  const Cut u = unit_cut<AL>(j, a.hidden);
+  const int parts = (end - 1) / kRun - stretch + 1;
+  const bool in = j * kU < a.hidden;
+  const Cut u = unit_cut<AC>(j, a.hidden);
   float sum[kU];
 #pragma unroll
   for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
-  unit_add<1>(sum, load_cut<1, AL>(g.part, ((int64_t)stretch * 2 + 1) * a.hidden, u));
-#pragma unroll 8
-  for (int s = stretch + 1; s <= last; ++s)
-    unit_add<1>(sum, load_cut<1, AL>(g.part, (int64_t)s * 2 * a.hidden, u));
-  put_row<TT, AL>(a, key, u, sum);
+  if (in) {
+#pragma unroll 4
+    for (int s = y; s < parts; s += 4)
+      unit_add<1>(sum, load_cut<1, AC>(g.part, ((int64_t)(stretch + s) * 2 + (s == 0 ? 1 : 0)) * a.hidden, u));
+  }
+  if (y > 0) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i) lds[y - 1][i][x] = sum[i];
+  }
+  __syncthreads();
+  if (y > 0 || !in) return;
+#pragma unroll
+  for (int i = 0; i < kU; ++i) sum[i] += lds[0][i][x] + (lds[1][i][x] + lds[2][i][x]);
+  put_row<TT, AC>(a, key, u, sum);
 }
 
 }  // namespace
@@ -313,15 +367,16 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g) {
 // ---------------------------------------------------------------- launches
 
 template <int DT, int G>
-static hipError_t embed_go(const EmbedArgs& args, bool al, hipStream_t s) {
+static hipError_t embed_go(const EmbedArgs& args, int access, hipStream_t s) {
   constexpr int64_t kMost = 1ll << 20;      // x blocks; with y the dispatch counts 32 bits of threads
   EmbedArgs a = args;
   const int units = (a.hidden + kU - 1) / kU, cols = (units + G - 1) / G;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMost, 0xFFFFFFFFll / 256 / cols));
-  for (; a.row0 < a.tokens; a.row0 += most * (256 / G)) {
-    const dim3 grid((unsigned)std::min<int64_t>(most, (a.tokens - a.row0 + 256 / G - 1) / (256 / G)), cols);
-    if (al) k_embed<DT, G, true><<<grid, 256, 0, s>>>(a);
-    else k_embed<DT, G, false><<<grid, 256, 0, s>>>(a);
+  for (; a.row0 < a.tokens; a.row0 += most * (256 / G) * 4) {
+    const dim3 grid((unsigned)std::min<int64_t>(most, (a.tokens - a.row0 + 256 / G * 4 - 1) / (256 / G * 4)), cols);
+    if (access == kStreamRows) k_embed<DT, G, kStreamRows><<<grid, 256, 0, s>>>(a);
+    else if (access == kAlignedRows) k_embed<DT, G, kAlignedRows><<<grid, 256, 0, s>>>(a);
+    else k_embed<DT, G, kOddRows><<<grid, 256, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -329,15 +384,15 @@ static hipError_t embed_go(const EmbedArgs& args, bool al, hipStream_t s) {
 }
 
 template <int DT>
-static hipError_t embed_size(const EmbedArgs& a, bool al, hipStream_t s) {
+static hipError_t embed_size(const EmbedArgs& a, int access, hipStream_t s) {
   const int units = (a.hidden + kU - 1) / kU;
-  return units <= 64 ? embed_go<DT, 64>(a, al, s) : embed_go<DT, 256>(a, al, s);
+  return units <= 64 ? embed_go<DT, 64>(a, access, s) : embed_go<DT, 256>(a, access, s);
 }
 
-hipError_t launch_embed(const EmbedArgs& a, int dtype, bool al, hipStream_t s) {
-  if (dtype == 1) return embed_size<1>(a, al, s);
-  if (dtype == 2) return embed_size<2>(a, al, s);
-  return embed_size<3>(a, al, s);
+hipError_t launch_embed(const EmbedArgs& a, int dtype, int access, hipStream_t s) {
+  if (dtype == 1) return embed_size<1>(a, access, s);
+  if (dtype == 2) return embed_size<2>(a, access, s);
+  return embed_size<3>(a, access, s);
 }
 
 // The workspace: sorted keys and positions (twice where the sort takes passes),
@@ -356,7 +411,8 @@ static int columns_of(int hidden) { return (hidden + 256 * kU - 1) / (256 * kU);
 // One dispatch counts threads in 32 bits.
 bool embed_bwd_fits(int64_t tokens, int vocab, int hidden) {
   return tokens < (1ll << 31) - kTile &&
-         stretches_of(tokens) * columns_of(hidden) + (vocab + kClear - 1) / kClear <= 0xFFFFFFFFll / 256;
+         stretches_of(tokens) * ((hidden + kJoinUnits * kU - 1) / (kJoinUnits * kU)) + (vocab + kClear - 1) / kClear <=
+             0xFFFFFFFFll / 256;
 }
 
 template <int DT, int TT>
@@ -367,9 +423,10 @@ static hipError_t runs_go(const EmbedBwdArgs& a, const RunArgs& g, bool al, hipS
   else k_embed_runs<DT, TT, false><<<grid, 256, 0, s>>>(a, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.stretches < 2) return e;
-  const unsigned join = (unsigned)((g.stretches - 1) * g.columns);
-  if (al) k_embed_join<TT, true><<<join, 256, 0, s>>>(a, g);
-  else k_embed_join<TT, false><<<join, 256, 0, s>>>(a, g);
+  const int columns = (a.hidden + kJoinUnits * kU - 1) / (kJoinUnits * kU);
+  const unsigned join = (unsigned)((g.stretches - 1) * columns);
+  if (al) k_embed_join<TT, true><<<join, 256, 0, s>>>(a, g, columns);
+  else k_embed_join<TT, false><<<join, 256, 0, s>>>(a, g, columns);
   return hipGetLastError();
 }
 
@@ -383,7 +440,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
   RunArgs g;
   g.part = reinterpret_cast<float*>(blocks ? hist + blocks * kBins : spare_keys);
   if (n > 0 && blocks == 0) {
-    k_sort_count<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, keys, pos);
+    k_sort_count<<<(unsigned)((n + 63) / 64), kCountThreads, 0, s>>>(a, keys, pos);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   } else if (n > 0) {
@@ -408,6 +465,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
   g.stretches = (int32_t)stretches_of(n);
   g.columns = columns_of(a.hidden);
   g.clears = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
+  g.per = n > 0 ? g.clears / (g.stretches * g.columns) : 0;
   if (dtype == 1) return runs_go<1, 1>(a, g, al, s);
   if (dtype == 2) return table_dtype == 1 ? runs_go<2, 1>(a, g, al, s) : runs_go<2, 2>(a, g, al, s);
   return table_dtype == 1 ? runs_go<3, 1>(a, g, al, s) : runs_go<3, 3>(a, g, al, s);

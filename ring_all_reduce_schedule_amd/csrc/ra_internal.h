@@ -101,7 +101,7 @@ int default_persistent_workgroups();
 // ---------------------------------------------------------------- row operators
 // What a tensor-parallel model does where it folds its ranks' buffers.  `al`:
 // every row of every array starts on a 16-byte boundary (and its length is a
-// multiple of 8).
+// multiple of 8).  `access`: an Access of ra_rows.h.
 
 struct NormArgs {
   RankPtrs in, out, scale;   // scale: used by 8-bit outputs
@@ -134,9 +134,10 @@ constexpr int kNormMaxHidden = 32768;
 // constant, so that the order in which dw is summed does not depend on the GPU.
 constexpr int kNormBwdBlocks = 512;
 
-hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, bool al, hipStream_t s);
+hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, int access, hipStream_t s);
 int norm_bwd_blocks(int64_t tokens);
-hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int h_dtype, float* dweight, bool al, hipStream_t s);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int h_dtype, float* dweight, int access,
+                           hipStream_t s);
 
 // How a length (a vocabulary) is cut over the ranks.
 struct Pieces {
@@ -182,7 +183,7 @@ struct EmbedArgs {
   int32_t p, vocab, hidden, n_out, ids64;
   float scale;
 };
-hipError_t launch_embed(const EmbedArgs& a, int dtype, bool al, hipStream_t s);
+hipError_t launch_embed(const EmbedArgs& a, int dtype, int access, hipStream_t s);
 
 struct EmbedBwdArgs {
   RankPtrs table;            // the ranks' gradients

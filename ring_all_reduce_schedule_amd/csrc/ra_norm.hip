@@ -34,16 +34,17 @@ __device__ __forceinline__ u32x2 unit_f8(const float* x) {
   return q;
 }
 
-template <bool AL>
+template <int AC>
 __device__ __forceinline__ void store_f8(void* p, int64_t row, const Cut& u, u32x2 q) {
   uint8_t* d = static_cast<uint8_t*>(p) + row + u.c;
-  if (AL || u.hi - u.lo == kU) {
-    if constexpr (AL) *reinterpret_cast<u32x2*>(d) = q;
+  if (AC != 0 || u.hi - u.lo == kU) {
+    if constexpr (AC == kStreamRows) __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(d));
+    else if constexpr (AC != 0) *reinterpret_cast<u32x2*>(d) = q;
     else *reinterpret_cast<u32x2_by1*>(d) = q;
   } else {
 #pragma unroll
     for (int k = 0; k < kU; ++k)
-      if (owns<AL>(u, k)) d[k] = (uint8_t)(q[k / 4] >> (k % 4 * 8));
+      if (owns<AC>(u, k)) d[k] = (uint8_t)(q[k / 4] >> (k % 4 * 8));
   }
 }
 
@@ -56,7 +57,7 @@ __device__ __forceinline__ float f8_amax(uint32_t bits) {
 
 // G threads to a row, K units to a thread: rows of up to 8 G K elements.
 // DT: the partials' type; RT: the residual's (0: none); F8: 8-bit output.
-template <int DT, int RT, int G, int K, bool F8, bool AL>
+template <int DT, int RT, int G, int K, bool F8, int AC>
 __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
   constexpr int kWaves = G / 64;
   __shared__ float lds_sum[16];
@@ -73,15 +74,15 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
   for (int k = 0; k < K; ++k) {
     const int j = tid + k * G;
     if (j * kU < hidden) {
-      const Cut u = unit_cut<AL>(j, hidden);
+      const Cut u = unit_cut<AC>(j, hidden);
       Unit<RT == 0 ? DT : RT> res{};
       if constexpr (RT != 0)
-        if (a.res) res = load_cut<RT, AL>(a.res, at, u);
-      fold_ranks<DT, AL>(h[k], a.in, a.p, at, u);
+        if (a.res) res = load_cut<RT, AC>(a.res, at, u);
+      fold_ranks<DT, AC>(h[k], a.in, a.p, at, u);
       if constexpr (RT != 0) {
 #pragma unroll
-        for (int i = 0; i < kU; ++i) h[k][i] += owns<AL>(u, i) ? unit_get<RT>(res, i) : 0.0f;
-        if (a.res_out) store_cut<RT, AL>(a.res_out, at, u, unit_make<RT>(h[k]));
+        for (int i = 0; i < kU; ++i) h[k][i] += owns<AC>(u, i) ? unit_get<RT>(res, i) : 0.0f;
+        if (a.res_out) store_cut<RT, AC>(a.res_out, at, u, unit_make<RT>(h[k]));
       }
 #pragma unroll
       for (int i = 0; i < kU; ++i) ss = __builtin_fmaf(h[k][i], h[k][i], ss);
@@ -96,19 +97,19 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
   for (int k = 0; k < K; ++k) {
     const int j = tid + k * G;
     const bool in = j * kU < hidden;
-    const Cut u = unit_cut<AL>(j, hidden);
+    const Cut u = unit_cut<AC>(j, hidden);
     uint32_t here = 0;
     if (in) {
-      const Unit<DT> w = load_cut<DT, AL>(a.weight, 0, u);
+      const Unit<DT> w = load_cut<DT, AC != 0>(a.weight, 0, u);
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        h[k][i] = owns<AL>(u, i) ? h[k][i] * rstd * unit_get<DT>(w, i) : 0.0f;
+        h[k][i] = owns<AC>(u, i) ? h[k][i] * rstd * unit_get<DT>(w, i) : 0.0f;
         const uint32_t m = __float_as_uint(h[k][i]) & 0x7fffffffu;
         here = here > m ? here : m;
       }
       if constexpr (!F8) {
         const Unit<DT> y = unit_make<DT>(h[k]);
-        for (int r = 0; r < a.n_out; ++r) store_cut<DT, AL>(a.out.b[r], at, u, y);
+        for (int r = 0; r < a.n_out; ++r) store_cut<DT, AC>(a.out.b[r], at, u, y);
       }
     }
     if constexpr (F8) {
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
           const u32x2 y = unit_f8(h[k]);
           const int groups = (hidden + a.group - 1) / a.group;
           for (int r = 0; r < a.n_out; ++r) {
-            store_f8<AL>(a.out.b[r], at, u, y);
+            store_f8<AC>(a.out.b[r], at, u, y);
             if (j * kU % a.group == 0)
               static_cast<float*>(a.scale.b[r])[row * groups + j * kU / a.group] = amax / kF8Max;
           }
@@ -142,11 +143,11 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
       if (j * kU < hidden) {
-        const Cut u = unit_cut<AL>(j, hidden);
+        const Cut u = unit_cut<AC>(j, hidden);
 #pragma unroll
         for (int i = 0; i < kU; ++i) h[k][i] *= inv;
         const u32x2 y = unit_f8(h[k]);
-        for (int r = 0; r < a.n_out; ++r) store_f8<AL>(a.out.b[r], at, u, y);
+        for (int r = 0; r < a.n_out; ++r) store_f8<AC>(a.out.b[r], at, u, y);
       }
     }
     // lanes of one wave: a row has at least 64 threads, and at most 64 ranks
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
 
 // Workgroups take the rows in a stride and keep their columns' sums for dw in
 // registers over all of them.
-template <int DT, int RT, int G, int K, bool AL>
+template <int DT, int RT, int G, int K, int AC>
 __global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
   constexpr int kWaves = G / 64;
   // Four units a thread leave no registers for h: it is read again, from the cache.
@@ -181,14 +182,14 @@ __global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
       if (j * kU < hidden) {
-        const Cut u = unit_cut<AL>(j, hidden);
+        const Cut u = unit_cut<AC>(j, hidden);
         Unit<RT>& hk = hu[kKeep ? k : 0];
-        hk = load_cut<RT, AL>(a.h, at, u);
-        const Unit<DT> w = load_cut<DT, AL>(a.weight, 0, u);
-        fold_ranks<DT, AL>(g[k], a.in, a.p, at, u);
+        hk = load_cut<RT, AC>(a.h, at, u);
+        const Unit<DT> w = load_cut<DT, AC != 0>(a.weight, 0, u);
+        fold_ranks<DT, AC>(g[k], a.in, a.p, at, u);
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
-          const float x = owns<AL>(u, i) ? unit_get<RT>(hk, i) * rstd : 0.0f;
+          const float x = owns<AC>(u, i) ? unit_get<RT>(hk, i) * rstd : 0.0f;
           dw[k][i] = __builtin_fmaf(g[k][i], x, dw[k][i]);
           g[k][i] *= unit_get<DT>(w, i);
           dot = __builtin_fmaf(g[k][i], x, dot);
@@ -201,20 +202,20 @@ __global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
       if (j * kU < hidden) {
-        const Cut u = unit_cut<AL>(j, hidden);
+        const Cut u = unit_cut<AC>(j, hidden);
         Unit<RT>& hk = hu[kKeep ? k : 0];
-        if constexpr (!kKeep) hk = load_cut<RT, AL>(a.h, at, u);
+        if constexpr (!kKeep) hk = load_cut<RT, AC>(a.h, at, u);
         Unit<RT> d{};
-        if (a.dh_in) d = load_cut<RT, AL>(a.dh_in, at, u);
+        if (a.dh_in) d = load_cut<RT, AC>(a.dh_in, at, u);
         float y[kU];
 #pragma unroll
         for (int i = 0; i < kU; ++i) {
           const float x = unit_get<RT>(hk, i) * rstd;
           y[i] = unit_get<RT>(d, i) + rstd * (g[k][i] - x * dot);
         }
-        store_cut<RT, AL>(a.dh, at, u, unit_make<RT>(y));
+        store_cut<RT, AC>(a.dh, at, u, unit_make<RT>(y));
         const Unit<DT> t = unit_make<DT>(y);
-        for (int r = 0; r < a.n_dx; ++r) store_cut<DT, AL>(a.dx.b[r], at, u, t);
+        for (int r = 0; r < a.n_dx; ++r) store_cut<DT, AC>(a.dx.b[r], at, u, t);
       }
     }
   }
@@ -223,7 +224,7 @@ __global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
       if (j * kU < hidden)
-        store_cut<1, AL>(a.part, (int64_t)blockIdx.x * hidden, unit_cut<AL>(j, hidden), unit_make<1>(dw[k]));
+        store_cut<1, AC != 0>(a.part, (int64_t)blockIdx.x * hidden, unit_cut<AC>(j, hidden), unit_make<1>(dw[k]));
     }
   }
 }
@@ -253,14 +254,15 @@ __global__ __launch_bounds__(1024) void k_norm_dweight(const float* part, float*
 
 // One launch, or several where the rows pass what one dispatch counts.
 template <int DT, int RT, int G, int K, bool F8>
-hipError_t norm_go(const NormArgs& args, bool al, hipStream_t s) {
+hipError_t norm_go(const NormArgs& args, int access, hipStream_t s) {
   constexpr int64_t kPer = G == 64 ? 4 : 1, kThreads = G == 64 ? 256 : G;
   constexpr int64_t kMost = 0xFFFFFFFFll / kThreads;
   NormArgs a = args;
   for (; a.row0 < a.tokens; a.row0 += kMost * kPer) {
     const dim3 grid((unsigned)std::min(kMost, (a.tokens - a.row0 + kPer - 1) / kPer)), block(kThreads);
-    if (al) k_norm<DT, RT, G, K, F8, true><<<grid, block, 0, s>>>(a);
-    else k_norm<DT, RT, G, K, F8, false><<<grid, block, 0, s>>>(a);
+    if (access == kStreamRows) k_norm<DT, RT, G, K, F8, kStreamRows><<<grid, block, 0, s>>>(a);
+    else if (access == kAlignedRows) k_norm<DT, RT, G, K, F8, kAlignedRows><<<grid, block, 0, s>>>(a);
+    else k_norm<DT, RT, G, K, F8, kOddRows><<<grid, block, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -268,68 +270,69 @@ hipError_t norm_go(const NormArgs& args, bool al, hipStream_t s) {
 }
 
 template <int DT, int RT, bool F8>
-hipError_t norm_size(const NormArgs& a, bool al, hipStream_t s) {
+hipError_t norm_size(const NormArgs& a, int access, hipStream_t s) {
   const int units = (a.hidden + kU - 1) / kU;
-  if (units <= 64) return norm_go<DT, RT, 64, 1, F8>(a, al, s);
-  if (units <= 256) return norm_go<DT, RT, 256, 1, F8>(a, al, s);
-  if (units <= 512) return norm_go<DT, RT, 512, 1, F8>(a, al, s);
-  if (units <= 1024) return norm_go<DT, RT, 1024, 1, F8>(a, al, s);
-  if (units <= 2048) return norm_go<DT, RT, 1024, 2, F8>(a, al, s);
-  return norm_go<DT, RT, 1024, 4, F8>(a, al, s);
+  if (units <= 64) return norm_go<DT, RT, 64, 1, F8>(a, access, s);
+  if (units <= 256) return norm_go<DT, RT, 256, 1, F8>(a, access, s);
+  if (units <= 512) return norm_go<DT, RT, 512, 1, F8>(a, access, s);
+  if (units <= 1024) return norm_go<DT, RT, 1024, 1, F8>(a, access, s);
+  if (units <= 2048) return norm_go<DT, RT, 1024, 2, F8>(a, access, s);
+  return norm_go<DT, RT, 1024, 4, F8>(a, access, s);
 }
 
 template <int DT, int RT>
-hipError_t norm_out(const NormArgs& a, bool f8, bool al, hipStream_t s) {
-  return f8 ? norm_size<DT, RT, true>(a, al, s) : norm_size<DT, RT, false>(a, al, s);
+hipError_t norm_out(const NormArgs& a, bool f8, int access, hipStream_t s) {
+  return f8 ? norm_size<DT, RT, true>(a, access, s) : norm_size<DT, RT, false>(a, access, s);
 }
 
 template <int DT>
-hipError_t norm_res(const NormArgs& a, int res_dtype, bool f8, bool al, hipStream_t s) {
-  if (!a.res && !a.res_out) return norm_out<DT, 0>(a, f8, al, s);
-  if (DT != 1 && res_dtype == 1) return norm_out<DT, 1>(a, f8, al, s);
-  return norm_out<DT, DT>(a, f8, al, s);
+hipError_t norm_res(const NormArgs& a, int res_dtype, bool f8, int access, hipStream_t s) {
+  if (!a.res && !a.res_out) return norm_out<DT, 0>(a, f8, access, s);
+  if (DT != 1 && res_dtype == 1) return norm_out<DT, 1>(a, f8, access, s);
+  return norm_out<DT, DT>(a, f8, access, s);
 }
 
 template <int DT, int RT, int G, int K>
-hipError_t bwd_go(const NormBwdArgs& a, bool al, int grid, hipStream_t s) {
-  if (al) k_norm_bwd<DT, RT, G, K, true><<<grid, G, 0, s>>>(a);
-  else k_norm_bwd<DT, RT, G, K, false><<<grid, G, 0, s>>>(a);
+hipError_t bwd_go(const NormBwdArgs& a, int access, int grid, hipStream_t s) {
+  if (access == kStreamRows) k_norm_bwd<DT, RT, G, K, kStreamRows><<<grid, G, 0, s>>>(a);
+  else if (access == kAlignedRows) k_norm_bwd<DT, RT, G, K, kAlignedRows><<<grid, G, 0, s>>>(a);
+  else k_norm_bwd<DT, RT, G, K, kOddRows><<<grid, G, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT, int RT>
-hipError_t bwd_size(const NormBwdArgs& a, bool al, int grid, hipStream_t s) {
+hipError_t bwd_size(const NormBwdArgs& a, int access, int grid, hipStream_t s) {
   const int units = (a.hidden + kU - 1) / kU;
-  if (units <= 64) return bwd_go<DT, RT, 64, 1>(a, al, grid, s);
-  if (units <= 256) return bwd_go<DT, RT, 256, 1>(a, al, grid, s);
-  if (units <= 512) return bwd_go<DT, RT, 512, 1>(a, al, grid, s);
-  if (units <= 1024) return bwd_go<DT, RT, 512, 2>(a, al, grid, s);
-  if (units <= 2048) return bwd_go<DT, RT, 1024, 2>(a, al, grid, s);
-  return bwd_go<DT, RT, 1024, 4>(a, al, grid, s);
+  if (units <= 64) return bwd_go<DT, RT, 64, 1>(a, access, grid, s);
+  if (units <= 256) return bwd_go<DT, RT, 256, 1>(a, access, grid, s);
+  if (units <= 512) return bwd_go<DT, RT, 512, 1>(a, access, grid, s);
+  if (units <= 1024) return bwd_go<DT, RT, 1024, 1>(a, access, grid, s);
+  if (units <= 2048) return bwd_go<DT, RT, 1024, 2>(a, access, grid, s);
+  return bwd_go<DT, RT, 1024, 4>(a, access, grid, s);
 }
 
 template <int DT>
-hipError_t bwd_res(const NormBwdArgs& a, int h_dtype, bool al, int grid, hipStream_t s) {
-  if (DT != 1 && h_dtype == 1) return bwd_size<DT, 1>(a, al, grid, s);
-  return bwd_size<DT, DT>(a, al, grid, s);
+hipError_t bwd_res(const NormBwdArgs& a, int h_dtype, int access, int grid, hipStream_t s) {
+  if (DT != 1 && h_dtype == 1) return bwd_size<DT, 1>(a, access, grid, s);
+  return bwd_size<DT, DT>(a, access, grid, s);
 }
 
 }  // namespace
 
-hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, bool al, hipStream_t s) {
-  if (dtype == 1) return norm_res<1>(a, res_dtype, f8, al, s);
-  if (dtype == 2) return norm_res<2>(a, res_dtype, f8, al, s);
-  return norm_res<3>(a, res_dtype, f8, al, s);
+hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, int access, hipStream_t s) {
+  if (dtype == 1) return norm_res<1>(a, res_dtype, f8, access, s);
+  if (dtype == 2) return norm_res<2>(a, res_dtype, f8, access, s);
+  return norm_res<3>(a, res_dtype, f8, access, s);
 }
 
 int norm_bwd_blocks(int64_t tokens) { return (int)std::min<int64_t>(tokens, kNormBwdBlocks); }
 
-hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int h_dtype, float* dweight, bool al, hipStream_t s) {
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, int h_dtype, float* dweight, int access, hipStream_t s) {
   const int grid = norm_bwd_blocks(a.tokens);
   if (grid > 0) {
-    hipError_t e = dtype == 1   ? bwd_res<1>(a, h_dtype, al, grid, s)
-                   : dtype == 2 ? bwd_res<2>(a, h_dtype, al, grid, s)
-                                : bwd_res<3>(a, h_dtype, al, grid, s);
+    hipError_t e = dtype == 1   ? bwd_res<1>(a, h_dtype, access, grid, s)
+                   : dtype == 2 ? bwd_res<2>(a, h_dtype, access, grid, s)
+                                : bwd_res<3>(a, h_dtype, access, grid, s);
     if (e != hipSuccess) return e;
   }
   if (dweight) {   // no rows: zeros

@@ -137,6 +137,9 @@ void debug_rows(const char* call, int p, int64_t tokens, int64_t cols, int dtype
                  (long long)tokens, (long long)cols, dtype, (int)al, (long long)extra);
 }
 
+// 0, 1, 2: odd rows, aligned rows, aligned rows of a call of `bytes` that streams.
+int access_of(bool al, int64_t bytes) { return !al ? 0 : bytes > ra::kStreamingBytes ? 2 : 1; }
+
 int launched(hipError_t e) { return e == hipSuccess ? RA_OK : fail_hip(e, "kernel launch"); }
 
 int check_workspace(Arrays* to, void* workspace, int64_t have, int64_t need) {
@@ -266,7 +269,9 @@ int ra_allreduce_rmsnorm(void* const* bufs, int p, int64_t tokens, int64_t hidde
   a.inv_h = 1.0f / (float)hidden;
   const bool al = all.al() && hidden % 8 == 0;
   debug_rows("allreduce_rmsnorm", p, tokens, hidden, dtype, al, 1);
-  return launched(ra::launch_norm(a, dtype, residual_dtype, f8, al, stream));
+  return launched(ra::launch_norm(
+      a, dtype, residual_dtype, f8, access_of(al, n * (p * e + (residual_in ? er : 0) + (residual_out ? er : 0) + n_out * eo)),
+      stream));
 }
 
 int ra_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes) {
@@ -327,7 +332,8 @@ int ra_allreduce_rmsnorm_backward(void* const* dys, int p, int64_t tokens, int64
   a.inv_h = 1.0f / (float)hidden;
   const bool al = all.al() && hidden % 8 == 0;
   debug_rows("allreduce_rmsnorm_backward", p, tokens, hidden, dtype, al, 1);
-  return launched(ra::launch_norm_bwd(a, dtype, h_dtype, dweight, al, stream));
+  return launched(ra::launch_norm_bwd(
+      a, dtype, h_dtype, dweight, access_of(al, n * (p * e + (dh_in ? 3 : 2) * eh + n_dx * e)), stream));
 }
 
 int ra_cross_entropy_workspace(int64_t tokens, int64_t vocab, int p, int64_t* bytes) {
@@ -425,7 +431,7 @@ int ra_embedding(const void* const* tables, int p, int64_t vocab, int64_t hidden
   a.scale = scale;
   const bool al = all.al() && hidden % 8 == 0;
   debug_rows("embedding", p, tokens, hidden, dtype, al, 1);
-  return launched(ra::launch_embed(a, dtype, al, stream));
+  return launched(ra::launch_embed(a, dtype, access_of(al, tokens * hidden * e * n_out), stream));
 }
 
 int ra_embedding_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes) {
