@@ -534,7 +534,7 @@ int ra_embedding(const void* const* tables, int p, int64_t vocab, int64_t hidden
 
 /*
  * ra_embedding_backward -- the gradient of the tables: dtable[v] = scale * the sum of dy
- * over the tokens with id v, added up in the order of their positions.
+ * over the tokens with id v, added up in an order that the ids alone decide.
  *   dy       [tokens][hidden] of `dtype`
  *   dtables  p arrays like the tables, of dtable_dtype (`dtype` or RA_FLOAT32)
  *   accumulate  0: every row is written, zeros where no token has it (with tokens ==
@@ -546,7 +546,7 @@ int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dt
                           const void* ids, int id_dtype, float scale, void* const* dtables, int p,
                           int64_t vocab, int dtable_dtype, int accumulate, void* workspace,
                           int64_t workspace_bytes, hipStream_t stream);
-int ra_embedding_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes);
+int ra_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden, int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -98,7 +98,7 @@ _SIGNATURES = {
     "ra_embedding": (_int, [_vp, _int, _i64, _i64, _int, _vp, _int, _i64, _f32, _vp, _int, _vp]),
     "ra_embedding_backward": (_int, [_vp, _i64, _i64, _int, _vp, _int, _f32, _vp, _int, _i64, _int,
                                      _int, _vp, _i64, _vp]),
-    "ra_embedding_backward_workspace": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "ra_embedding_backward_workspace": (_int, [_i64, _i64, _i64, ctypes.POINTER(_i64)]),
 }
 
 
@@ -141,19 +141,28 @@ def _check(code):
 
 # ---------------------------------------------------------------- marshalling
 
+_torch_module = None
+_codes = {}
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _codes.update({torch.int32: RA_INT32, torch.float32: RA_FLOAT32,
+                       torch.bfloat16: RA_BFLOAT16, torch.float16: RA_FLOAT16,
+                       torch.float64: RA_FLOAT64, torch.int64: RA_INT64})
+        _torch_module = torch
+    return _torch_module
 
 
 def dtype_code(t):
-    torch = _torch()
-    codes = {torch.int32: RA_INT32, torch.float32: RA_FLOAT32, torch.bfloat16: RA_BFLOAT16,
-             torch.float16: RA_FLOAT16, torch.float64: RA_FLOAT64, torch.int64: RA_INT64}
-    if t.dtype not in codes:
+    _torch()
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype} "
                         "(int32, int64, float16, bfloat16, float32, float64)")
-    return codes[t.dtype]
+    return code
 
 
 def _stream_handle(stream, device):
@@ -363,12 +372,24 @@ def _table(what, tensors, numel, dtype, dev):
     return array.array("Q", [t.data_ptr() for t in tensors])
 
 
-def _tables_of(what, tensors, numels, dtype, dev):
-    """The same for tensors of different lengths."""
-    for t, n in zip(tensors, numels):
-        if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-            _refuse(what, t, n, dtype, dev)
-    return array.array("Q", [t.data_ptr() for t in tensors])
+def _cut_table(what, tensors, dim, other):
+    """(table, total): the same for matrices that are the ranks' pieces of a length, cut along
+    `dim` as ra_chunk_bounds cuts it; `other` is their other dimension."""
+    t0 = tensors[0]
+    dtype, dev = t0.dtype, t0.get_device()
+    sizes = []
+    for t in tensors:
+        shape = t.shape
+        if len(shape) != 2 or shape[1 - dim] != other:
+            raise ValueError(f"{what} must be matrices with {other} in dimension {1 - dim}")
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _refuse(what, t, t.numel(), dtype, dev)
+        sizes.append(shape[dim])
+    total, p = sum(sizes), len(sizes)
+    base, extra = divmod(total, p)
+    if sizes != [base + 1] * extra + [base] * (p - extra):
+        raise ValueError(f"{what}: {sizes} is not how ra_chunk_bounds cuts {total} over {p} ranks")
+    return array.array("Q", [t.data_ptr() for t in tensors]), total
 
 
 def _address(table):
@@ -441,10 +462,11 @@ def ra_cross_entropy_workspace(tokens, vocab, p):
     return n.value
 
 
-def ra_embedding_backward_workspace(tokens, hidden):
+def ra_embedding_backward_workspace(tokens, vocab, hidden):
     """Bytes of workspace (host only)."""
     n = ctypes.c_int64()
-    _check(lib().ra_embedding_backward_workspace(int(tokens), int(hidden), ctypes.byref(n)))
+    _check(lib().ra_embedding_backward_workspace(int(tokens), int(vocab), int(hidden),
+                                                 ctypes.byref(n)))
     return n.value
 
 
@@ -512,39 +534,31 @@ def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), 
     _run_on(dev, stream, lib().ra_allreduce_rmsnorm_backward, args)
 
 
-def _index_code(what, t):
+def _index(what, t, tokens, dev):
+    """(address, dtype code) of token numbers."""
     torch = _torch()
-    if t.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"{what} must be int32 or int64, not {t.dtype}")
-    return dtype_code(t)
-
-
-def _pieces(what, tensors, dim):
-    """Total length of `dim` over the ranks, checked to be cut as ra_chunk_bounds cuts it."""
-    sizes = [t.shape[dim] for t in tensors]
-    total, p = sum(sizes), len(sizes)
-    base, extra = divmod(total, p)
-    if any(s != base + (r < extra) for r, s in enumerate(sizes)):
-        raise ValueError(f"{what}: {sizes} is not how ra_chunk_bounds cuts {total} over {p} ranks")
-    return total
+    dtype = t.dtype
+    if dtype is not torch.int64 and dtype is not torch.int32:
+        raise TypeError(f"{what} must be int32 or int64, not {dtype}")
+    return _arg(what, t, tokens, dtype, dev), _codes[dtype]
 
 
 def _xent_args(logits, targets, grads):
-    """(first tensor, tables to keep, arguments up to dtype, targets' arguments, grads' address,
-    tokens, vocab, device index)."""
+    """(first tensor, tables to keep, targets' arguments, tokens, vocab, device index)."""
     x0 = _first("logits", logits)
-    tokens, dev, dtype = targets.numel(), x0.get_device(), x0.dtype
-    if any(t.dim() != 2 or t.shape[0] != tokens for t in logits):
-        raise ValueError("logits must be [tokens, columns of the rank]")
-    vocab = _pieces("logits", logits, 1)
-    numels = [t.numel() for t in logits]
-    table, grad_table = _tables_of("logits", logits, numels, dtype, dev), None
+    tokens, dev = targets.numel(), x0.get_device()
+    table, vocab = _cut_table("logits", logits, 1, tokens)
+    grad_table = None
     if grads is not None:
-        if len(grads) != len(logits) or any(g.shape != t.shape for g, t in zip(grads, logits)):
+        if len(grads) != len(logits):
+            raise ValueError("grads must be as many as the logits")
+        g0 = _first("grads", grads)
+        if g0.dtype is not x0.dtype or g0.get_device() != dev:
+            _refuse("grads", g0, g0.numel(), x0.dtype, dev)
+        grad_table, columns = _cut_table("grads", grads, 1, tokens)
+        if columns != vocab:
             raise ValueError("grads must have the logits' shapes")
-        grad_table = _tables_of("grads", grads, numels, dtype, dev)
-    goal = (_arg("targets", targets, tokens, targets.dtype, dev), _index_code("targets", targets))
-    return x0, (table, grad_table), goal, tokens, vocab, dev
+    return x0, (table, grad_table), _index("targets", targets, tokens, dev), tokens, vocab, dev
 
 
 def ra_cross_entropy(logits, targets, loss=None, lse=None, grads=None, dloss=None, grad_scale=1.0,
@@ -575,39 +589,28 @@ def ra_cross_entropy_backward(logits, targets, lse, grads, dloss=None, grad_scal
     _run_on(dev, stream, lib().ra_cross_entropy_backward, args)
 
 
-def _cut_table(what, tables):
-    """(first tensor, pointer table, vocab, hidden, device index) of a table's pieces."""
-    t0 = _first(what, tables)
-    hidden = t0.shape[-1] if t0.dim() == 2 else 0
-    if any(t.dim() != 2 or t.shape[1] != hidden for t in tables):
-        raise ValueError(f"{what} must be [rows of the rank, hidden]")
-    dev = t0.get_device()
-    table = _tables_of(what, tables, [t.numel() for t in tables], t0.dtype, dev)
-    return t0, table, _pieces(what, tables, 0), hidden, dev
-
-
 def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
     """outs = scale times the rows of a table cut over the ranks; see include/ra.h.
 
     tables: a list of [rows of the rank, hidden] tensors."""
-    t0, table, vocab, hidden, dev = _cut_table("tables", tables)
-    tokens = ids.numel()
+    t0 = _first("tables", tables)
+    hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
+    table, vocab = _cut_table("tables", tables, 0, hidden)
     _first("outs", outs)
     out_table = _table("outs", outs, tokens * hidden, t0.dtype, dev)
     args = (_address(table), len(table), vocab, hidden, dtype_code(t0),
-            _arg("ids", ids, tokens, ids.dtype, dev), _index_code("ids", ids), tokens, scale,
-            _address(out_table), len(out_table))
+            *_index("ids", ids, tokens, dev), tokens, scale, _address(out_table), len(out_table))
     _run_on(dev, stream, lib().ra_embedding, args)
 
 
 def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspace=None, stream=None):
     """dtables = (or with accumulate +=) scale times the sums of dy's rows by token; see
     include/ra.h."""
-    t0, table, vocab, hidden, dev = _cut_table("dtables", dtables)
-    tokens = ids.numel()
+    t0 = _first("dtables", dtables)
+    hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
+    table, vocab = _cut_table("dtables", dtables, 0, hidden)
     keep, wp, wn = _workspace(workspace, t0, stream, lib().ra_embedding_backward_workspace,
-                              tokens, hidden)
+                              tokens, vocab, hidden)
     args = (_arg("dy", dy, tokens * hidden, dy.dtype, dev), tokens, hidden, dtype_code(dy),
-            _arg("ids", ids, tokens, ids.dtype, dev), _index_code("ids", ids), scale,
-            _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
+            *_index("ids", ids, tokens, dev), scale, _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
     _run_on(dev, stream, lib().ra_embedding_backward, args)

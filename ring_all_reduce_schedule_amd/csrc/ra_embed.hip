@@ -212,12 +212,15 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
 // Sorted positions of one stretch, and rows that one workgroup clears.
 constexpr int kRun = 16, kClear = 8;
 
+// Two launches after the sort's: the stretches' runs, together with zeros for the
+// rows that have no tokens; then the runs that cross stretches.
 struct RunArgs {
   const int* keys;
   const int* pos;
-  float* part;       // [stretches][2][hidden]: a stretch's first and last run, where they cross its ends
-  int32_t sorted;    // positions
-  int32_t stretches, clears, columns, per;   // workgroups: stretches * columns and clears
+  float* part;        // [stretches][2][hidden]: a stretch's first and last run, where they cross its ends
+  int32_t sorted;     // positions
+  int32_t stretches;
+  int32_t columns;    // workgroups to a stretch, of 256 units
 };
 
 template <int TT, int AC>
@@ -252,71 +255,74 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int key) {
   return lo;
 }
 
+// Zeros for those of rows [v0, v0 + kClear) that no token has.  A workgroup to
+// eight rows (131,072 rows of 16 KiB, with the runs of 16384 tokens beside them,
+// 400 us; four rows 415).  A bit for each row, set by a launch before, in place of the
+// search here, and a workgroup to a row took 443 us for the zeros alone: a
+// workgroup that waits for one load has to write more than a few KiB.
+template <int TT, int AC>
+__device__ __forceinline__ void clear_rows(const EmbedBwdArgs& a, const RunArgs& g, int v0) {
+  __shared__ int taken[kClear];
+  const int v1 = min(a.vocab, v0 + kClear);
+  if (threadIdx.x < kClear) taken[threadIdx.x] = 0;
+  __syncthreads();
+  const int from = lower_bound(g.keys, g.sorted, v0), to = lower_bound(g.keys, g.sorted, v1);
+  for (int i = from + (int)threadIdx.x; i < to; i += 256) taken[g.keys[i] - v0] = 1;
+  __syncthreads();
+  for (int v = v0; v < v1; ++v) {
+    if (taken[v - v0]) continue;
+    const int r = piece_of(a.cut, v);
+    const int64_t row = (int64_t)(v - piece_lo(a.cut, r)) * a.hidden;
+    if constexpr (AC != 0) {
+      // 16 bytes a lane, next to each other
+      u32x4* at = reinterpret_cast<u32x4*>(static_cast<char*>(a.table.b[r]) + row * ElemSize<TT>::value);
+      for (int j = threadIdx.x; j < a.hidden / (16 / ElemSize<TT>::value); j += 256) at[j] = u32x4{0, 0, 0, 0};
+    } else {
+      for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
+        store_cut<TT, AC>(a.table.b[r], row, unit_cut<AC>(j, a.hidden), Unit<TT>{});
+    }
+  }
+}
+
 template <int DT, int TT, int AC>
 __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
-  // Workgroups that add up runs wait for scattered rows, those that clear rows only
-  // write: one of the former to every g.per of the latter keeps the memory busy.
-  const int runs = g.stretches * g.columns, turn = (int)blockIdx.x / (g.per + 1);
-  const bool run = turn < runs && (int)blockIdx.x % (g.per + 1) == 0;
-  if (!run) {
-    // rows no token has: zeros
-    __shared__ int taken[kClear];
-    const int v0 = ((int)blockIdx.x - min(turn + 1, runs)) * kClear;
-    const int v1 = min(a.vocab, v0 + kClear);
-    if (threadIdx.x < kClear) taken[threadIdx.x] = 0;
-    __syncthreads();
-    const int from = lower_bound(g.keys, g.sorted, v0), to = lower_bound(g.keys, g.sorted, v1);
-    for (int i = from + (int)threadIdx.x; i < to; i += 256) taken[g.keys[i] - v0] = 1;
-    __syncthreads();
-    const Unit<TT> zero{};
-    for (int v = v0; v < v1; ++v) {
-      if (taken[v - v0]) continue;
-      const int r = piece_of(a.cut, v);
-      const int64_t row = (int64_t)(v - piece_lo(a.cut, r)) * a.hidden;
-      if constexpr (AC != 0) {
-        // 16 bytes a lane, next to each other
-        u32x4* at = reinterpret_cast<u32x4*>(static_cast<char*>(a.table.b[r]) + row * ElemSize<TT>::value);
-        for (int j = threadIdx.x; j < a.hidden / (16 / ElemSize<TT>::value); j += 256) at[j] = u32x4{0, 0, 0, 0};
-      } else {
-        for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
-          store_cut<TT, AC>(a.table.b[r], row, unit_cut<AC>(j, a.hidden), zero);
-      }
-    }
+  const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
+  if (stretch >= g.stretches) {
+    clear_rows<TT, AC>(a, g, ((int)blockIdx.x - g.stretches * g.columns) * kClear);
     return;
   }
-  const int stretch = turn / g.columns, j = turn % g.columns * 256 + threadIdx.x;
-  const int lo = stretch * kRun, hi = min(g.sorted, lo + kRun);
+  const int lo = stretch * kRun, n = min(g.sorted - lo, kRun), lane = threadIdx.x % 64;
+  // the stretch's keys with the one before and the one behind, and its positions:
+  // one load each, a lane to a key
+  const int near = lo - 1 + lane;
+  const int keys = lane < n + 2 && near >= 0 && near < g.sorted ? g.keys[near] : -1;
+  const int places = lane < n ? g.pos[lo + lane] : 0;
   if (j * kU >= a.hidden) return;
   const Cut u = unit_cut<AC>(j, a.hidden);
   // all the stretch's rows at once
   Unit<DT> rows[kRun];
 #pragma unroll
   for (int k = 0; k < kRun; ++k)
-    if (lo + k < hi) rows[k] = load_cut<DT, AC>(a.dy, (int64_t)g.pos[lo + k] * a.hidden, u);
-  const int before = lo > 0 ? g.keys[lo - 1] : -1, after = hi < g.sorted ? g.keys[hi] : -1;
+    rows[k] = load_cut<DT, AC>(a.dy, (int64_t)__builtin_amdgcn_readlane(places, k < n ? k : 0) * a.hidden, u);
   float sum[kU];
 #pragma unroll
   for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
-  int start = lo;
+  bool open = __builtin_amdgcn_readlane(keys, 0) == __builtin_amdgcn_readlane(keys, 1);   // began earlier
 #pragma unroll
   for (int k = 0; k < kRun; ++k) {
-    if (lo + k < hi) {
-      const int key = g.keys[lo + k];
-      if (key < a.vocab) {
-        unit_add<DT>(sum, rows[k]);
-        const bool last = lo + k + 1 == hi;
-        if (last || g.keys[lo + k + 1] != key) {
-          const bool open_before = start == lo && before == key, open_after = last && after == key;
-          if (open_before || open_after) {
-            const int64_t slot = ((int64_t)stretch * 2 + (open_before ? 0 : 1)) * a.hidden;
-            store_cut<1, AC>(g.part, slot, u, unit_make<1>(sum));
-          } else {
-            put_row<TT, AC>(a, key, u, sum);
-          }
-          start = lo + k + 1;
-#pragma unroll
-          for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
+    const int key = __builtin_amdgcn_readlane(keys, k + 1), next = __builtin_amdgcn_readlane(keys, k + 2);
+    if (k < n && key < a.vocab) {
+      unit_add<DT>(sum, rows[k]);
+      if (k + 1 == n || next != key) {
+        if (open || next == key) {
+          const int64_t slot = ((int64_t)stretch * 2 + (open ? 0 : 1)) * a.hidden;
+          store_cut<1, AC>(g.part, slot, u, unit_make<1>(sum));
+        } else {
+          put_row<TT, AC>(a, key, u, sum);
         }
+        open = false;
+#pragma unroll
+        for (int i = 0; i < kU; ++i) sum[i] = 0.0f;
       }
     }
   }
@@ -328,8 +334,9 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
 // frequent token has many.
 constexpr int kJoinUnits = 64;
 template <int TT, int AC>
-__global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g, int columns) {
+__global__ __launch_bounds__(256) void k_embed_join(EmbedBwdArgs a, RunArgs g) {
   __shared__ float lds[3][kU][kJoinUnits];
+  const int columns = (a.hidden + kJoinUnits * kU - 1) / (kJoinUnits * kU);
   const int stretch = blockIdx.x / columns, x = threadIdx.x % kJoinUnits, y = threadIdx.x / kJoinUnits;
   const int j = blockIdx.x % columns * kJoinUnits + x;
   const int lo = stretch * kRun, hi = lo + kRun;
@@ -406,27 +413,27 @@ int64_t embed_bwd_words(int64_t tokens, int hidden) {
   return (blocks ? 4 : 2) * up4(tokens) + blocks * kBins + stretches_of(tokens) * 2 * hidden;
 }
 
-static int columns_of(int hidden) { return (hidden + 256 * kU - 1) / (256 * kU); }
+static int columns_of(int hidden, int units) { return (hidden + units * kU - 1) / (units * kU); }
 
 // One dispatch counts threads in 32 bits.
 bool embed_bwd_fits(int64_t tokens, int vocab, int hidden) {
   return tokens < (1ll << 31) - kTile &&
-         stretches_of(tokens) * ((hidden + kJoinUnits * kU - 1) / (kJoinUnits * kU)) + (vocab + kClear - 1) / kClear <=
+         stretches_of(tokens) * columns_of(hidden, kJoinUnits) + (vocab + kClear - 1) / kClear <=
              0xFFFFFFFFll / 256;
 }
 
 template <int DT, int TT>
 static hipError_t runs_go(const EmbedBwdArgs& a, const RunArgs& g, bool al, hipStream_t s) {
-  const unsigned grid = (unsigned)(g.stretches * g.columns + g.clears);
+  const int clears = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
+  const unsigned grid = (unsigned)(g.stretches * g.columns + clears);
   if (grid == 0) return hipSuccess;
-  if (al) k_embed_runs<DT, TT, true><<<grid, 256, 0, s>>>(a, g);
-  else k_embed_runs<DT, TT, false><<<grid, 256, 0, s>>>(a, g);
+  if (al) k_embed_runs<DT, TT, kAlignedRows><<<grid, 256, 0, s>>>(a, g);
+  else k_embed_runs<DT, TT, kOddRows><<<grid, 256, 0, s>>>(a, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.stretches < 2) return e;
-  const int columns = (a.hidden + kJoinUnits * kU - 1) / (kJoinUnits * kU);
-  const unsigned join = (unsigned)((g.stretches - 1) * columns);
-  if (al) k_embed_join<TT, true><<<join, 256, 0, s>>>(a, g, columns);
-  else k_embed_join<TT, false><<<join, 256, 0, s>>>(a, g, columns);
+  const unsigned joins = (unsigned)((g.stretches - 1) * columns_of(a.hidden, kJoinUnits));
+  if (al) k_embed_join<TT, kAlignedRows><<<joins, 256, 0, s>>>(a, g);
+  else k_embed_join<TT, kOddRows><<<joins, 256, 0, s>>>(a, g);
   return hipGetLastError();
 }
 
@@ -437,7 +444,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
   int* spare_keys = pos + up4(n);
   int* spare_pos = spare_keys + up4(n);
   int* hist = spare_pos + up4(n);
-  RunArgs g;
+  RunArgs g = {};
   g.part = reinterpret_cast<float*>(blocks ? hist + blocks * kBins : spare_keys);
   if (n > 0 && blocks == 0) {
     k_sort_count<<<(unsigned)((n + 63) / 64), kCountThreads, 0, s>>>(a, keys, pos);
@@ -463,9 +470,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
   g.pos = pos;
   g.sorted = (int32_t)n;
   g.stretches = (int32_t)stretches_of(n);
-  g.columns = columns_of(a.hidden);
-  g.clears = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
-  g.per = n > 0 ? g.clears / (g.stretches * g.columns) : 0;
+  g.columns = columns_of(a.hidden, 256);
   if (dtype == 1) return runs_go<1, 1>(a, g, al, s);
   if (dtype == 2) return table_dtype == 1 ? runs_go<2, 1>(a, g, al, s) : runs_go<2, 2>(a, g, al, s);
   return table_dtype == 1 ? runs_go<3, 1>(a, g, al, s) : runs_go<3, 3>(a, g, al, s);

@@ -434,9 +434,10 @@ int ra_embedding(const void* const* tables, int p, int64_t vocab, int64_t hidden
   return launched(ra::launch_embed(a, dtype, access_of(al, tokens * hidden * e * n_out), stream));
 }
 
-int ra_embedding_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes) {
+int ra_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden, int64_t* bytes) {
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
   int rc = check_rows(tokens, hidden, ra::kEmbedMaxHidden, "hidden");
+  if (rc == RA_OK) rc = check_rows(0, vocab, ra::kXentMaxVocab, "vocab");
   if (rc == RA_OK) *bytes = ra::embed_bwd_words(tokens, (int)hidden) * 4;
   return rc;
 }

@@ -86,7 +86,7 @@ def test_embedding_backward(p, t, v, h, dt, tt, kind, off, accumulate):
     assert torch.equal(got[rest], old[rest] if accumulate else torch.zeros_like(old[rest]))
     for c, flat in tables:
         untouched(flat, off, c.numel())
-    # the same bits again: the order of the sums is that of the positions
+    # the same bits again: the ids alone decide the order of the sums
     again = cut(old, p, off)
     B.ra_embedding_backward(dy, ids, [c[0] for c in again], scale=1.5, accumulate=accumulate)
     assert all(torch.equal(a[0], b[0]) for a, b in zip(tables, again))

@@ -223,7 +223,7 @@ def test_workspace_of_the_callers():
     g = torch.Generator(device="cuda").manual_seed(8)
     dy, ids = torch.randn((9000, 40), device="cuda", generator=g), torch.randint(0, 90, (9000,), device="cuda", generator=g)
     a, b = torch.empty((90, 40), device="cuda"), torch.empty((90, 40), device="cuda")
-    n = B.ra_embedding_backward_workspace(9000, 40)
+    n = B.ra_embedding_backward_workspace(9000, 90, 40)
     flat = torch.full((n + 64,), 0xAB, dtype=torch.uint8, device="cuda")
     B.ra_embedding_backward(dy, ids, [a])
     B.ra_embedding_backward(dy, ids, [b], workspace=flat[:n])

@@ -173,21 +173,21 @@ def test_workspace_sizes():
     for t in (1, 7, 512, 513, 1 << 20):
         assert B.ra_rmsnorm_backward_workspace(t, 1000) <= 512 * 1000 * 4
         assert B.ra_rmsnorm_backward_workspace(t, 1000) >= 4000
-        assert B.ra_embedding_backward_workspace(t, 64) >= 8 * t
+        assert B.ra_embedding_backward_workspace(t, 100, 64) >= 8 * t
         assert B.ra_cross_entropy_workspace(t, 128000, 8) >= 0
-    assert B.ra_embedding_backward_workspace(0, 64) == 0
     assert B.ra_cross_entropy_workspace(1 << 20, 128000, 8) == 0
     assert B.ra_cross_entropy_workspace(8, 32768, 2) > 100
     for f, args in ((B.ra_rmsnorm_backward_workspace, (-1, 8)), (B.ra_rmsnorm_backward_workspace, (1, 0)),
                     (B.ra_cross_entropy_workspace, (1, 0, 2)), (B.ra_cross_entropy_workspace, (1, 8, 0)),
-                    (B.ra_embedding_backward_workspace, (1, -3))):
+                    (B.ra_embedding_backward_workspace, (1, 5, -3)),
+                    (B.ra_embedding_backward_workspace, (1, 0, 3))):
         with pytest.raises(B.RaError) as e:
             f(*args)
         assert e.value.code == INV
     lib = B.lib()
     assert lib.ra_rmsnorm_backward_workspace(1, 8, None) == INV
     assert lib.ra_cross_entropy_workspace(1, 8, 1, None) == INV
-    assert lib.ra_embedding_backward_workspace(1, 8, None) == INV
+    assert lib.ra_embedding_backward_workspace(1, 8, 8, None) == INV
 
 
 def test_other_calls_do_not_take_the_8_bit_type():
@@ -211,10 +211,11 @@ def test_binding_refuses_host_tensors():
 
 
 def test_pieces_have_to_be_cut_as_the_library_cuts_them():
-    class Shape:
-        def __init__(self, *s):
-            self.shape = s
-    assert B._pieces("t", [Shape(1, 4), Shape(1, 3), Shape(1, 3)], 1) == 10
-    for sizes in ((3, 4, 3), (5, 3, 2), (4, 4, 2)):
+    def cut(*sizes):
+        return B._cut_table("t", [torch.zeros(2, n) for n in sizes], 1, 2)[1]
+    assert cut(4, 3, 3) == 10 and cut(2, 2) == 4 and cut(1, 0, 0) == 1
+    for sizes in ((3, 4, 3), (5, 3, 2), (4, 4, 2), (0, 1)):
         with pytest.raises(ValueError):
-            B._pieces("t", [Shape(1, s) for s in sizes], 1)
+            cut(*sizes)
+    with pytest.raises(ValueError):
+        B._cut_table("t", [torch.zeros(2, 3), torch.zeros(3, 3)], 1, 2)
