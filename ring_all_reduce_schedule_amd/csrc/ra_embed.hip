@@ -103,10 +103,12 @@ __global__ __launch_bounds__(kCountThreads) void k_sort_count(EmbedBwdArgs a, in
 }
 
 // More: passes over digits of kBits bits, lowest first, each a stable counting
-// sort of blocks of kTile keys.
-constexpr int kBits = 9, kBins = 1 << kBits, kSortThreads = 512, kTile = 4096;
-constexpr int kPerLane = kTile / kSortThreads;      // 8
+// sort of blocks of PER * kSortThreads keys.  A block looks through the counts of
+// all blocks, so large calls take larger ones; small ones, with two keys to a
+// thread, put more compute units to work.
+constexpr int kBits = 9, kBins = 1 << kBits, kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSmallTile = 2 * kSortThreads, kLargeTile = 8 * kSortThreads, kSmallMost = 1 << 16;
 
 // Key and position number i of a pass's input; the first pass reads the tokens.
 struct SortIn {
@@ -114,19 +116,20 @@ struct SortIn {
   const int* pos;
 };
 
+template <int PER>
 __global__ __launch_bounds__(kSortThreads) void k_sort_hist(EmbedBwdArgs a, SortIn in, int shift, int* hist) {
   __shared__ int bins[kBins];
   for (int i = threadIdx.x; i < kBins; i += kSortThreads) bins[i] = 0;
   __syncthreads();
-  const int64_t lo = (int64_t)blockIdx.x * kTile;
-  int key[kPerLane];
+  const int64_t lo = (int64_t)blockIdx.x * (PER * kSortThreads);
+  int key[PER];
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) {
+  for (int k = 0; k < PER; ++k) {
     const int64_t i = min(lo + k * kSortThreads + threadIdx.x, a.tokens - 1);
     key[k] = in.keys ? in.keys[i] : key_of(a, i);
   }
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k)
+  for (int k = 0; k < PER; ++k)
     if (lo + k * kSortThreads + threadIdx.x < a.tokens) atomicAdd(&bins[(key[k] >> shift) & (kBins - 1)], 1);
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kSortThreads) hist[(int64_t)blockIdx.x * kBins + i] = bins[i];
@@ -135,17 +138,18 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_hist(EmbedBwdArgs a, Sort
 // A block's keys go behind all keys of lower digits, and behind the earlier
 // blocks' keys of the same digit; inside the block wave by wave (a wave has
 // neighbouring keys), inside a wave round by round and lane by lane.
+template <int PER>
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, SortIn in, int shift,
                                                              const int* hist, int blocks, int* keys, int* pos) {
   __shared__ int place[kSortWaves][kBins];   // keys of a digit in a wave, then where they start
-  __shared__ int total[kBins];
+  __shared__ int waves[kSortWaves];          // sums of the digits' counts, by wave
   const int tid = threadIdx.x, w = tid / 64, lane = tid % 64;
   static_assert(kSortThreads == kBins, "a thread to a digit");
   // digit tid: how many keys there are, and how many in earlier blocks
-  const int64_t lo = (int64_t)blockIdx.x * kTile + w * (kTile / kSortWaves);
-  int key[kPerLane], rank[kPerLane], from[kPerLane];
+  const int64_t lo = ((int64_t)blockIdx.x * kSortWaves + w) * (PER * 64);
+  int key[PER], rank[PER], from[PER];
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) {
+  for (int k = 0; k < PER; ++k) {
     const int64_t i = min(lo + k * 64 + lane, a.tokens - 1);
     key[k] = in.keys ? in.keys[i] : key_of(a, i);
     from[k] = in.pos ? in.pos[i] : (int)i;
@@ -158,17 +162,20 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
     all += n;
   }
   for (int i = 0; i < kSortWaves; ++i) place[i][tid] = 0;
-  total[tid] = all;
-  __syncthreads();
-  // sum over the lower digits
-  for (int d = 1; d < kBins; d *= 2) {
-    const int add = tid >= d ? total[tid - d] : 0;
-    __syncthreads();
-    total[tid] += add;
-    __syncthreads();
-  }
+  // sum over the lower digits: in the wave, then of the waves before
+  int lower_digits = all;
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) {
+  for (int d = 1; d < 64; d *= 2) {
+    const int add = __shfl_up(lower_digits, d);
+    lower_digits += lane >= d ? add : 0;
+  }
+  if (lane == 63) waves[w] = lower_digits;
+  lower_digits -= all;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortWaves; ++i) lower_digits += i < w ? waves[i] : 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
     const bool in_range = lo + k * 64 + lane < a.tokens;
     const int digit = (key[k] >> shift) & (kBins - 1);
     uint64_t same = __ballot(in_range);
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   __syncthreads();
-  int at = (tid > 0 ? total[tid - 1] : 0) + before;
+  int at = lower_digits + before;
   for (int i = 0; i < kSortWaves; ++i) {
     const int n = place[i][tid];
     place[i][tid] = at;
@@ -198,7 +205,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kPerLane; ++k) {
+  for (int k = 0; k < PER; ++k) {
     if (lo + k * 64 + lane < a.tokens) {
       const int to = place[w][(key[k] >> shift) & (kBins - 1)] + rank[k];
       keys[to] = key[k];
@@ -405,7 +412,10 @@ hipError_t launch_embed(const EmbedArgs& a, int dtype, int access, hipStream_t s
 // The workspace: sorted keys and positions (twice where the sort takes passes),
 // the passes' counts, the open runs' sums.  Each part starts on 16 bytes.
 static int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
-static int sort_blocks(int64_t tokens) { return tokens <= kCountMost ? 0 : (int)((tokens + kTile - 1) / kTile); }
+static int tile_of(int64_t tokens) { return tokens <= kSmallMost ? kSmallTile : kLargeTile; }
+static int sort_blocks(int64_t tokens) {
+  return tokens <= kCountMost ? 0 : (int)((tokens + tile_of(tokens) - 1) / tile_of(tokens));
+}
 static int64_t stretches_of(int64_t tokens) { return (tokens + kRun - 1) / kRun; }
 
 int64_t embed_bwd_words(int64_t tokens, int hidden) {
@@ -417,7 +427,7 @@ static int columns_of(int hidden, int units) { return (hidden + units * kU - 1) 
 
 // One dispatch counts threads in 32 bits.
 bool embed_bwd_fits(int64_t tokens, int vocab, int hidden) {
-  return tokens < (1ll << 31) - kTile &&
+  return tokens < (1ll << 31) - kLargeTile &&
          stretches_of(tokens) * columns_of(hidden, kJoinUnits) + (vocab + kClear - 1) / kClear <=
              0xFFFFFFFFll / 256;
 }
@@ -455,8 +465,13 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
     while ((a.vocab >> bits) != 0) ++bits;          // keys are 0 .. vocab
     SortIn in = {nullptr, nullptr};
     for (int shift = 0; shift < bits; shift += kBits) {
-      k_sort_hist<<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist);
-      k_sort_place<<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist, (int)blocks, keys, pos);
+      if (tile_of(n) == kSmallTile) {
+        k_sort_hist<2><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist);
+        k_sort_place<2><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist, (int)blocks, keys, pos);
+      } else {
+        k_sort_hist<8><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist);
+        k_sort_place<8><<<(unsigned)blocks, kSortThreads, 0, s>>>(a, in, shift, hist, (int)blocks, keys, pos);
+      }
       hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
       in = {keys, pos};
