@@ -55,15 +55,15 @@ __device__ __forceinline__ float f8_amax(uint32_t bits) {
   return bits < __float_as_uint(kAmaxFloor) ? kAmaxFloor : __uint_as_float(bits);
 }
 
-// G threads to a row, K units to a thread: rows of up to 8 G K elements.
-// DT: the partials' type; RT: the residual's (0: none); F8: 8-bit output.
-template <int DT, int RT, int G, int K, bool F8, int AC>
-__global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
-  constexpr int kWaves = G / 64;
+// ONE: a wave to a row, four rows to a workgroup; else a workgroup to a row.  K units
+// to a thread.  DT: the partials' type; RT: the residual's (0: none); F8: 8-bit output.
+template <int DT, int RT, bool ONE, int K, bool F8, int AC>
+__global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm(NormArgs a) {
+  const int G = ONE ? 64 : blockDim.x;
   __shared__ float lds_sum[16];
   __shared__ uint32_t lds_max[16];
-  const int64_t row = a.row0 + (G == 64 ? (int64_t)blockIdx.x * 4 + threadIdx.x / 64 : (int64_t)blockIdx.x);
-  const int tid = G == 64 ? threadIdx.x % 64 : threadIdx.x;
+  const int64_t row = a.row0 + (ONE ? (int64_t)blockIdx.x * 4 + threadIdx.x / 64 : (int64_t)blockIdx.x);
+  const int tid = ONE ? threadIdx.x % 64 : threadIdx.x;
   if (row >= a.tokens) return;      // whole waves; only where there is no barrier
   const int hidden = a.hidden;
   const int64_t at = row * hidden;
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
       for (int i = 0; i < kU; ++i) ss = __builtin_fmaf(h[k][i], h[k][i], ss);
     }
   }
-  ss = block_sum<kWaves>(ss, lds_sum);
+  ss = ONE ? wave_sum(ss) : block_sum(ss, lds_sum, G / 64);
   const float rstd = 1.0f / __builtin_sqrtf(ss * a.inv_h + a.eps);
   if (tid == 0 && a.rstd) a.rstd[row] = rstd;
 
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
   }
   if constexpr (F8) {
     if (a.group) return;
-    const float amax = f8_amax(block_max_u32<kWaves>(top, lds_max)), inv = kF8Max / amax;
+    const float amax = f8_amax(ONE ? wave_max_u32(top) : block_max_u32(top, lds_max, G / 64)), inv = kF8Max / amax;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
@@ -159,9 +159,9 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_norm(NormArgs a) {
 
 // Workgroups take the rows in a stride and keep their columns' sums for dw in
 // registers over all of them.
-template <int DT, int RT, int G, int K, int AC>
-__global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
-  constexpr int kWaves = G / 64;
+template <int DT, int RT, int K, int AC>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a) {
+  const int G = blockDim.x;
   // Four units a thread leave no registers for h: it is read again, from the cache.
   constexpr bool kKeep = K <= 2;
   __shared__ float lds_sum[2][16];
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(G) void k_norm_bwd(NormBwdArgs a) {
       }
     }
     // two buffers in turn: a wave may be a row ahead of another's last read
-    dot = block_sum<kWaves>(dot, lds_sum[turn]) * a.inv_h;
+    dot = block_sum(dot, lds_sum[turn], G / 64) * a.inv_h;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int j = tid + k * G;
@@ -252,17 +252,20 @@ __global__ __launch_bounds__(1024) void k_norm_dweight(const float* part, float*
 
 // ---------------------------------------------------------------- launches
 
+// Threads that hold `units` units, K to a thread.
+int threads_for(int units, int K) { return (units + 64 * K - 1) / (64 * K) * 64; }
+
 // One launch, or several where the rows pass what one dispatch counts.
-template <int DT, int RT, int G, int K, bool F8>
-hipError_t norm_go(const NormArgs& args, int access, hipStream_t s) {
-  constexpr int64_t kPer = G == 64 ? 4 : 1, kThreads = G == 64 ? 256 : G;
-  constexpr int64_t kMost = 0xFFFFFFFFll / kThreads;
+template <int DT, int RT, bool ONE, int K, bool F8>
+hipError_t norm_go(const NormArgs& args, int units, int access, hipStream_t s) {
+  const int64_t per = ONE ? 4 : 1, threads = ONE ? 256 : threads_for(units, K);
+  const int64_t most = 0xFFFFFFFFll / threads;
   NormArgs a = args;
-  for (; a.row0 < a.tokens; a.row0 += kMost * kPer) {
-    const dim3 grid((unsigned)std::min(kMost, (a.tokens - a.row0 + kPer - 1) / kPer)), block(kThreads);
-    if (access == kStreamRows) k_norm<DT, RT, G, K, F8, kStreamRows><<<grid, block, 0, s>>>(a);
-    else if (access == kAlignedRows) k_norm<DT, RT, G, K, F8, kAlignedRows><<<grid, block, 0, s>>>(a);
-    else k_norm<DT, RT, G, K, F8, kOddRows><<<grid, block, 0, s>>>(a);
+  for (; a.row0 < a.tokens; a.row0 += most * per) {
+    const dim3 grid((unsigned)std::min(most, (a.tokens - a.row0 + per - 1) / per)), block((unsigned)threads);
+    if (access == kStreamRows) k_norm<DT, RT, ONE, K, F8, kStreamRows><<<grid, block, 0, s>>>(a);
+    else if (access == kAlignedRows) k_norm<DT, RT, ONE, K, F8, kAlignedRows><<<grid, block, 0, s>>>(a);
+    else k_norm<DT, RT, ONE, K, F8, kOddRows><<<grid, block, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -272,12 +275,10 @@ hipError_t norm_go(const NormArgs& args, int access, hipStream_t s) {
 template <int DT, int RT, bool F8>
 hipError_t norm_size(const NormArgs& a, int access, hipStream_t s) {
   const int units = (a.hidden + kU - 1) / kU;
-  if (units <= 64) return norm_go<DT, RT, 64, 1, F8>(a, access, s);
-  if (units <= 256) return norm_go<DT, RT, 256, 1, F8>(a, access, s);
-  if (units <= 512) return norm_go<DT, RT, 512, 1, F8>(a, access, s);
-  if (units <= 1024) return norm_go<DT, RT, 1024, 1, F8>(a, access, s);
-  if (units <= 2048) return norm_go<DT, RT, 1024, 2, F8>(a, access, s);
-  return norm_go<DT, RT, 1024, 4, F8>(a, access, s);
+  if (units <= 64) return norm_go<DT, RT, true, 1, F8>(a, units, access, s);
+  if (units <= 1024) return norm_go<DT, RT, false, 1, F8>(a, units, access, s);
+  if (units <= 2048) return norm_go<DT, RT, false, 2, F8>(a, units, access, s);
+  return norm_go<DT, RT, false, 4, F8>(a, units, access, s);
 }
 
 template <int DT, int RT>
@@ -292,23 +293,21 @@ hipError_t norm_res(const NormArgs& a, int res_dtype, bool f8, int access, hipSt
   return norm_out<DT, DT>(a, f8, access, s);
 }
 
-template <int DT, int RT, int G, int K>
-hipError_t bwd_go(const NormBwdArgs& a, int access, int grid, hipStream_t s) {
-  if (access == kStreamRows) k_norm_bwd<DT, RT, G, K, kStreamRows><<<grid, G, 0, s>>>(a);
-  else if (access == kAlignedRows) k_norm_bwd<DT, RT, G, K, kAlignedRows><<<grid, G, 0, s>>>(a);
-  else k_norm_bwd<DT, RT, G, K, kOddRows><<<grid, G, 0, s>>>(a);
+template <int DT, int RT, int K>
+hipError_t bwd_go(const NormBwdArgs& a, int units, int access, int grid, hipStream_t s) {
+  const int threads = threads_for(units, K);
+  if (access == kStreamRows) k_norm_bwd<DT, RT, K, kStreamRows><<<grid, threads, 0, s>>>(a);
+  else if (access == kAlignedRows) k_norm_bwd<DT, RT, K, kAlignedRows><<<grid, threads, 0, s>>>(a);
+  else k_norm_bwd<DT, RT, K, kOddRows><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <int DT, int RT>
 hipError_t bwd_size(const NormBwdArgs& a, int access, int grid, hipStream_t s) {
   const int units = (a.hidden + kU - 1) / kU;
-  if (units <= 64) return bwd_go<DT, RT, 64, 1>(a, access, grid, s);
-  if (units <= 256) return bwd_go<DT, RT, 256, 1>(a, access, grid, s);
-  if (units <= 512) return bwd_go<DT, RT, 512, 1>(a, access, grid, s);
-  if (units <= 1024) return bwd_go<DT, RT, 1024, 1>(a, access, grid, s);
-  if (units <= 2048) return bwd_go<DT, RT, 1024, 2>(a, access, grid, s);
-  return bwd_go<DT, RT, 1024, 4>(a, access, grid, s);
+  if (units <= 1024) return bwd_go<DT, RT, 1>(a, units, access, grid, s);
+  if (units <= 2048) return bwd_go<DT, RT, 2>(a, units, access, grid, s);
+  return bwd_go<DT, RT, 4>(a, units, access, grid, s);
 }
 
 template <int DT>

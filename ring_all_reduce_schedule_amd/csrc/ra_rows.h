@@ -261,29 +261,21 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t x) {
   return max_u32(max_u32(a, b), max_u32(c, d));
 }
 
-// Sum over the WAVES waves of a workgroup, the same in every lane.  `lds` holds
-// WAVES floats of this call alone until every wave has passed the next barrier.
-template <int WAVES>
-__device__ __forceinline__ float block_sum(float x, float* lds) {
+// Over the workgroup's `waves` waves (at most 16), the same in every lane.  `lds` is
+// this call's alone until every wave has passed the next barrier.
+__device__ __forceinline__ float block_sum(float x, float* lds, int waves) {
   x = wave_sum(x);
-  if constexpr (WAVES == 1) return x;
   if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
   __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) s += lds[w];
-  return s;
+  const int lane = threadIdx.x % 16;
+  return lane_value(row_sum(lane < waves ? lds[lane] : 0.0f), 0);
 }
-template <int WAVES>
-__device__ __forceinline__ uint32_t block_max_u32(uint32_t x, uint32_t* lds) {
+__device__ __forceinline__ uint32_t block_max_u32(uint32_t x, uint32_t* lds, int waves) {
   x = wave_max_u32(x);
-  if constexpr (WAVES == 1) return x;
   if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
   __syncthreads();
-  uint32_t s = 0;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) s = s > lds[w] ? s : lds[w];
-  return s;
+  const int lane = threadIdx.x % 16;
+  return (uint32_t)__builtin_amdgcn_readlane((int)row_max_u32(lane < waves ? lds[lane] : 0u), 0);
 }
 
 }  // namespace ra
