@@ -165,7 +165,7 @@ struct XentArgs {
 };
 
 // Workgroups that share a row, 1 where a workgroup takes a whole row.
-int xent_splits(int64_t tokens, int vocab, int p);
+int xent_splits(int64_t tokens, int vocab, int p, bool grad);
 void xent_geometry(XentArgs* a);
 int64_t xent_words(int64_t tokens, int splits);   // 32-bit words of workspace
 

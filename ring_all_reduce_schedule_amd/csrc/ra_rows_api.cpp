@@ -153,8 +153,8 @@ int64_t norm_bwd_bytes(int64_t tokens, int64_t hidden) {
   return (int64_t)ra::norm_bwd_blocks(tokens) * hidden * (int64_t)sizeof(float);
 }
 
-int64_t xent_bytes(int64_t tokens, int64_t vocab, int p) {
-  return ra::xent_words(tokens, ra::xent_splits(tokens, (int)vocab, p)) * (int64_t)sizeof(float);
+int64_t xent_bytes(int64_t tokens, int64_t vocab, int p, bool grad) {
+  return ra::xent_words(tokens, ra::xent_splits(tokens, (int)vocab, p, grad)) * (int64_t)sizeof(float);
 }
 
 // Logits and gradients of a cross entropy, and what both directions need of them.
@@ -340,7 +340,7 @@ int ra_cross_entropy_workspace(int64_t tokens, int64_t vocab, int p, int64_t* by
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
   int rc = check_ranks(p);
   if (rc == RA_OK) rc = check_rows(tokens, vocab, ra::kXentMaxVocab, "vocab");
-  if (rc == RA_OK) *bytes = xent_bytes(tokens, vocab, p);
+  if (rc == RA_OK) *bytes = std::max(xent_bytes(tokens, vocab, p, false), xent_bytes(tokens, vocab, p, true));
   return rc;
 }
 
@@ -360,13 +360,13 @@ int ra_cross_entropy(void* const* logits, int p, int64_t tokens, int64_t vocab, 
   rc = add_xent(&all, &a, logits, grads, vocab, valid, dtype, targets, target_dtype, dloss, grad_scale);
   if (rc == RA_OK) rc = all.add("loss", -1, loss, tokens * 4, 4, true, true, 1);
   if (rc == RA_OK) rc = all.add("lse", -1, lse, tokens * 4, 4, true, true, 1);
-  if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, xent_bytes(tokens, vocab, p));
+  if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, xent_bytes(tokens, vocab, p, grads != nullptr));
   if (rc == RA_OK) rc = all.overlaps();
   if (rc != RA_OK) return rc;
   a.loss = loss;
   a.lse = lse;
   a.part = static_cast<float*>(workspace);
-  a.splits = ra::xent_splits(tokens, (int)vocab, p);
+  a.splits = ra::xent_splits(tokens, (int)vocab, p, grads != nullptr);
   const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
   debug_rows("cross_entropy", p, tokens, vocab, dtype, al, a.splits);
   return launched(ra::launch_xent(a, dtype, grads != nullptr, al, stream));

@@ -676,11 +676,18 @@ void xent_geometry(XentArgs* a) {
 
 int64_t xent_words(int64_t tokens, int splits) { return splits > 1 ? tokens * (kRowSum + 2 * splits) : 0; }
 
-int xent_splits(int64_t tokens, int vocab, int p) {
-  // To be shared, a row needs two chunks for each wave of its workgroups.
-  const int64_t most = std::min<int64_t>(64, total_chunks(vocab, p) / (2 * kSplitWaves));
-  if (tokens >= 512 || most < 2 || vocab / p < kU) return 1;
-  return (int)std::min<int64_t>(most, (1024 + tokens - 1) / tokens);
+// Sharing a row costs a second launch, and a third and another look at the logits
+// for the gradient.  Measured (8 ranks, bfloat16, us; shared / a workgroup to a row):
+//   loss      128000 columns: 1 token 5.6 / 12.7, 128 11.9 / 13.5, 192 15.7 / 13.5
+//              64000: 1 token 5.5 / 8.1, 64 8.9 / 8.5;  32000: 1 token 5.4 / 5.3
+//   gradient  128000: 1 token 9.4 / 20.6, 128 25.4 / 24.8;  32000: 64 11.8 / 13.6, 128 16.6 / 14.6
+//               8192: 1 token 8.1 / 9.3, 192 9.9 / 10.0
+int xent_splits(int64_t tokens, int vocab, int p, bool grad) {
+  const int chunks = total_chunks(vocab, p);
+  if (vocab / p < kU || (grad ? tokens > 96 : chunks <= 64 || tokens > chunks / 2)) return 1;
+  // two chunks at least for each wave of a row's workgroups
+  const int64_t most = std::min<int64_t>(64, chunks / (2 * kSplitWaves));
+  return most < 2 ? 1 : (int)std::min<int64_t>(most, (1024 + tokens - 1) / tokens);
 }
 
 hipError_t launch_xent(const XentArgs& a, int dtype, bool grad, bool al, hipStream_t s) {

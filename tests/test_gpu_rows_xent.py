@@ -36,6 +36,8 @@ CASES = [
     (8, 4, 128000, 128000, "f16", 0), (9, 2, 50017, 50001, "f32", 0), (8, 65, 32768, 32768, "bf16", 0),
     (8, 512, 16384, 16384, "bf16", 0), (8, 512, 16384, 16380, "f32", 3), (4, 514, 32768, 32768, "f16", 0),
     (4, 514, 33000, 33000, "f32", 0), (8, 512, 65536, 65536, "bf16", 0), (3, 513, 70001, 70000, "bf16", 0),
+    (8, 96, 40000, 39990, "bf16", 0), (8, 97, 40000, 39990, "f16", 0), (3, 130, 70001, 70000, "bf16", 0),
+    (5, 40, 66001, 66001, "f32", 1), (8, 300, 128000, 128000, "bf16", 0), (2, 61, 16390, 16390, "f16", 0),
     (8, 512, 131072, 131072, "bf16", 0), (1, 512, 151_937, 151_900, "f16", 0), (2, 512, 140_000, 140_000, "f32", 0),
 ]
 
