@@ -420,7 +420,7 @@ __global__ __launch_bounds__(G) void k_xent_loss(XentArgs a) {
   if (threadIdx.x == 0) write_loss(a, row, t.y, xy, sum);
 }
 
-// The loss and the gradient: workgroups take rows in a stride.  Each wave keeps its
+// The loss and the gradient: a workgroup to a row, or to rows in a stride.  Each wave keeps its
 // first K whole chunks of a row in registers, and one more of any kind (what is
 // left of a piece, in general); any others it reads again for the gradient.  As
 // soon as a unit's gradient is made, its registers take the next row's unit, and
@@ -599,11 +599,13 @@ int compute_units() {
   return n;
 }
 
-// As many workgroups of `waves` waves as the GPU holds at once: 16 waves of up to
-// 128 registers to a compute unit.
+// Workgroups that leave room for no other on a compute unit stay and take rows in a
+// stride; smaller ones take a row each, and the next one's loads cover this one's
+// arithmetic (2^30 bfloat16 logits, us, a row each / staying: 4096 columns 779 / 927,
+// 16384 796 / 848, 65536 781 / 826, 131072 841 / 832).
 template <int DT, int K, int MODE>
 hipError_t row_go(const XentArgs& a, int waves, hipStream_t s) {
-  const int64_t most = (int64_t)compute_units() * (16 / waves);
+  const int64_t most = waves > 8 ? compute_units() : 0xFFFFFFFFll / (waves * 64);
   k_xent<DT, K, MODE><<<(unsigned)std::min(most, a.tokens), waves * 64, 0, s>>>(a);
   return hipGetLastError();
 }
