@@ -451,7 +451,8 @@ int ra_stream_copy_resident(void* dst, const void* src, int64_t bytes, int grid,
  *   rstd          1 / sqrt(mean(h^2) + eps), [tokens] float32, or NULL; the backward
  *                 call wants it
  *   eps           > 0 and finite, so that a row of zeros gives zeros
- * hidden is at most 32768.
+ * hidden is at most 32768.  The squares are float32: rows with |h| beyond 1e19 / sqrt(hidden)
+ * overflow, and give zeros.
  */
 int ra_allreduce_rmsnorm(void* const* bufs, int p, int64_t tokens, int64_t hidden, int dtype,
                          const void* residual_in, void* residual_out, int residual_dtype,
@@ -473,14 +474,14 @@ int ra_allreduce_rmsnorm(void* const* bufs, int p, int64_t tokens, int64_t hidde
  *            is dh for each of them.  Each may be one of dys.
  *   dweight  [hidden] float32, or NULL.  With tokens == 0 it gets zeros.  Its sum over
  *            the tokens has a fixed order.
- *   workspace  ra_rmsnorm_backward_workspace bytes where dweight is wanted
+ *   workspace  ra_allreduce_rmsnorm_backward_workspace bytes where dweight is wanted
  */
 int ra_allreduce_rmsnorm_backward(void* const* dys, int p, int64_t tokens, int64_t hidden,
                                   int dtype, const void* h, int h_dtype, const float* rstd,
                                   const void* weight, const void* dh_in, void* dh,
                                   void* const* dxs, int n_dx, float* dweight, void* workspace,
                                   int64_t workspace_bytes, hipStream_t stream);
-int ra_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes);
+int ra_allreduce_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes);
 
 /*
  * ra_cross_entropy -- softmax cross entropy of logits whose vocabulary is cut over

@@ -89,7 +89,7 @@ _SIGNATURES = {
                                     _int, _int, _vp, _int, _vp, _vp]),
     "ra_allreduce_rmsnorm_backward": (_int, [_vp, _int, _i64, _i64, _int, _vp, _int, _vp, _vp, _vp,
                                              _vp, _vp, _int, _vp, _vp, _i64, _vp]),
-    "ra_rmsnorm_backward_workspace": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
+    "ra_allreduce_rmsnorm_backward_workspace": (_int, [_i64, _i64, ctypes.POINTER(_i64)]),
     "ra_cross_entropy": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _vp, _vp, _vp, _vp,
                                 _f32, _vp, _i64, _vp]),
     "ra_cross_entropy_workspace": (_int, [_i64, _i64, _int, ctypes.POINTER(_i64)]),
@@ -448,10 +448,10 @@ def _workspace(workspace, like, stream, size_call, *sizes):
     return workspace, workspace.data_ptr(), n.value
 
 
-def ra_rmsnorm_backward_workspace(tokens, hidden):
+def ra_allreduce_rmsnorm_backward_workspace(tokens, hidden):
     """Bytes of workspace (host only)."""
     n = ctypes.c_int64()
-    _check(lib().ra_rmsnorm_backward_workspace(int(tokens), int(hidden), ctypes.byref(n)))
+    _check(lib().ra_allreduce_rmsnorm_backward_workspace(int(tokens), int(hidden), ctypes.byref(n)))
     return n.value
 
 
@@ -525,8 +525,8 @@ def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), 
     dx_table = _table("dxs", dxs, n, d0.dtype, dev)
     keep, wp, wn = None, None, 0
     if dweight is not None:
-        keep, wp, wn = _workspace(workspace, d0, stream, lib().ra_rmsnorm_backward_workspace,
-                                  tokens, hidden)
+        keep, wp, wn = _workspace(workspace, d0, stream,
+                                  lib().ra_allreduce_rmsnorm_backward_workspace, tokens, hidden)
     args = (at, p, tokens, hidden, code, _arg("h", h, n, h.dtype, dev), dtype_code(h),
             _arg("rstd", rstd, tokens, f32, dev), _arg("weight", weight, hidden, d0.dtype, dev),
             _arg("dh_in", dh_in, n, h.dtype, dev), _arg("dh", dh, n, h.dtype, dev),

@@ -274,7 +274,7 @@ int ra_allreduce_rmsnorm(void* const* bufs, int p, int64_t tokens, int64_t hidde
       stream));
 }
 
-int ra_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes) {
+int ra_allreduce_rmsnorm_backward_workspace(int64_t tokens, int64_t hidden, int64_t* bytes) {
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
   int rc = check_rows(tokens, hidden, ra::kNormMaxHidden, "hidden");
   if (rc == RA_OK) *bytes = norm_bwd_bytes(tokens, hidden);

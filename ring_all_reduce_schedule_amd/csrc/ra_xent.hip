@@ -21,7 +21,17 @@
 // once is all it cannot avoid, so a workgroup keeps as much of its row in
 // registers as they hold and only what is beyond that is read a second time.  Next
 // comes arithmetic, two exponentials for each logit above all, which is why the
-// other operations on a logit are kept to a handful.
+// other operations on a logit are kept to a handful.  Measured on MI355X, where a
+// copy of 8 GiB runs at 6.55 TB/s:
+//   8192 x 131072 bfloat16, 8 ranks, with gradient   832 us, 5.2 TB/s
+//   ... the loss alone                               353 us, 6.1 TB/s
+//   ... the gradient alone, from lse                 750 us, 5.7 TB/s
+//   1003 x 50017 float32, 9 ranks, with gradient      98 us, 4.1 TB/s
+//   4 x 128000 bfloat16, the loss alone              7.0 us in two launches
+// The first took 847 us with the arithmetic left out, the same with the logits in
+// one buffer, and 4% more with half of each row read twice: a row of 256 KiB to a
+// compute unit keeps 256 rows' worth of DRAM pages open where a copy moves through
+// memory in order, and that is what is left.  Rows of 8192 columns reach 5.6 TB/s.
 #include "ra_rows.h"
 
 namespace ra {

@@ -169,15 +169,15 @@ def test_pieces_without_columns_may_be_null():
 
 
 def test_workspace_sizes():
-    assert B.ra_rmsnorm_backward_workspace(0, 128) == 0
+    assert B.ra_allreduce_rmsnorm_backward_workspace(0, 128) == 0
     for t in (1, 7, 512, 513, 1 << 20):
-        assert B.ra_rmsnorm_backward_workspace(t, 1000) <= 512 * 1000 * 4
-        assert B.ra_rmsnorm_backward_workspace(t, 1000) >= 4000
+        assert B.ra_allreduce_rmsnorm_backward_workspace(t, 1000) <= 512 * 1000 * 4
+        assert B.ra_allreduce_rmsnorm_backward_workspace(t, 1000) >= 4000
         assert B.ra_embedding_backward_workspace(t, 100, 64) >= 8 * t
         assert B.ra_cross_entropy_workspace(t, 128000, 8) >= 0
     assert B.ra_cross_entropy_workspace(1 << 20, 128000, 8) == 0
     assert B.ra_cross_entropy_workspace(8, 32768, 2) > 100
-    for f, args in ((B.ra_rmsnorm_backward_workspace, (-1, 8)), (B.ra_rmsnorm_backward_workspace, (1, 0)),
+    for f, args in ((B.ra_allreduce_rmsnorm_backward_workspace, (-1, 8)), (B.ra_allreduce_rmsnorm_backward_workspace, (1, 0)),
                     (B.ra_cross_entropy_workspace, (1, 0, 2)), (B.ra_cross_entropy_workspace, (1, 8, 0)),
                     (B.ra_embedding_backward_workspace, (1, 5, -3)),
                     (B.ra_embedding_backward_workspace, (1, 0, 3))):
@@ -185,7 +185,7 @@ def test_workspace_sizes():
             f(*args)
         assert e.value.code == INV
     lib = B.lib()
-    assert lib.ra_rmsnorm_backward_workspace(1, 8, None) == INV
+    assert lib.ra_allreduce_rmsnorm_backward_workspace(1, 8, None) == INV
     assert lib.ra_cross_entropy_workspace(1, 8, 1, None) == INV
     assert lib.ra_embedding_backward_workspace(1, 8, 8, None) == INV
 
