@@ -13,7 +13,7 @@
 // largest logit.  Partial sums keep the c they are relative to, and two of them
 // join as z = z1 2^(c1 - c) + z2 2^(c2 - c) with exact differences.
 //
-// That holds as long as z is neither 0 nor beyond float32.  A row where it is --
+// That holds as long as z stays inside float32's range.  A row where it does not --
 // every column -inf or masked with the type's lowest value, a NaN or +inf, logits
 // beyond 10^9 or so -- is done again with the largest logit subtracted first.
 //
@@ -287,7 +287,8 @@ __device__ __forceinline__ Part plain_part(const XentArgs& a, int64_t row) {
   return {m, wave_sum(z)};
 }
 
-__device__ __forceinline__ bool usable(Part t) { return t.z > 0.0f && t.z < INFINITY; }
+// Whether z is well inside float32's range; NaN is not.
+__device__ __forceinline__ bool usable(Part t) { return t.z > 0x1p-100f && t.z < 0x1p120f; }
 __device__ __forceinline__ bool empty(const Sum& t) { return t.plain && t.c == -INFINITY && t.z == 0.0f; }
 
 // The loss is taken from z and c - x_y log2 e, and not from lse, which loses z in a
@@ -390,7 +391,7 @@ __device__ __forceinline__ void take_rest(Part& part, const XentArgs& a, int64_t
 }
 
 // Writes the gradient of those chunks, reading them again.
-template <int DT, int MODE>
+template <int DT, int MODE, bool PLAIN>
 __device__ __forceinline__ void grad_rest(const XentArgs& a, int64_t row, int q0, int step, int end, const Token& t,
                                           const Grad& g) {
   for (; q0 < end; q0 += kMore * step) {
@@ -400,8 +401,8 @@ __device__ __forceinline__ void grad_rest(const XentArgs& a, int64_t row, int q0
     for (int k = 0; k < kMore; ++k) {
       const int q = q0 + k * step;
       if (q >= end) continue;
-      if (q < a.full) write_grad<DT, MODE, true, false>(v[k], chunk(a, q), a, row, t, g);
-      else write_grad<DT, MODE, false, false>(v[k], chunk(a, q), a, row, t, g);
+      if (q < a.full) write_grad<DT, MODE, true, PLAIN>(v[k], chunk(a, q), a, row, t, g);
+      else write_grad<DT, MODE, false, PLAIN>(v[k], chunk(a, q), a, row, t, g);
     }
   }
 }
@@ -494,7 +495,7 @@ __global__ __launch_bounds__(1024) void k_xent(XentArgs a) {
       }
       if (more < end) {
         write_grad<DT, MODE, false, false>(v[0], chunk(a, more), a, row, t, g);
-        grad_rest<DT, MODE>(a, row, rest, waves, end, t, g);
+        grad_rest<DT, MODE, false>(a, row, rest, waves, end, t, g);
       }
       if (next >= a.tokens) return;
       v[0] = fetch<DT, MODE>(a, next, chunk(a, min(more, end - 1)));
@@ -572,10 +573,10 @@ __global__ __launch_bounds__(kSplitThreads) void k_xent_grad(XentArgs a) {
   const Token t = token(a, row);
   Sum sum;
   if constexpr (FROM_LSE) {
-    // e^lse is the sum; beyond 2^100, and where it is no number, relative to it
+    // e^lse is the sum.  x - lse is taken first: a product lse log2 e would be
+    // rounded once more, and nothing here makes up for that.
     const float lse = a.lse_in[row];
-    const bool plain = !(__builtin_fabsf(lse) < 0x1p100f);
-    sum = {plain ? lse : lse * kLog2e, lse == -INFINITY ? 0.0f : 1.0f, plain};
+    sum = {lse, lse == -INFINITY ? 0.0f : 1.0f, lse == -INFINITY};
   } else {
     const float* space = row_space(a, row);
     sum = {space[0], space[1], space[2] != 0.0f};
@@ -583,7 +584,7 @@ __global__ __launch_bounds__(kSplitThreads) void k_xent_grad(XentArgs a) {
   const Grad g = grad_of(t, sum);
   const int w = lo + wave_id();
   if (other_grad<DT, MODE>(a, row, w, kSplitWaves, hi, t, g)) return;
-  grad_rest<DT, MODE>(a, row, w, kSplitWaves, hi, t, g);
+  grad_rest<DT, MODE, FROM_LSE>(a, row, w, kSplitWaves, hi, t, g);
 }
 
 template <int DT, int G, int MODE>

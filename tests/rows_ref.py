@@ -125,7 +125,10 @@ def xent(x, targets, valid, dloss, grad_scale):
     grad[targets >= valid] = math.nan
     grad[:, valid:] = 0.0
     cc = c.abs().unsqueeze(1)
-    egrad = cc * (share * ((6 + 2 * far) * U + ez) + 3 * U * one) + U * grad.abs()
+    # the exponential gives 0 below float32's smallest normal number, 2^-126, relative to a z that
+    # is at least 2 to the minus rounding of m log2 e (u of itself), and never below 2^-100
+    flushed = 2.0 ** -126 * torch.exp2((at.abs() * 1.45 * U).clamp_max(100.0))
+    egrad = cc * (share * ((6 + 2 * far) * U + ez) + 3 * U * one + flushed) + U * grad.abs()
     zero = torch.zeros_like
     return (loss, lse, grad, torch.where(eloss.isfinite(), eloss, zero(eloss)),
             torch.where(elses.isfinite(), elses, zero(elses)), torch.where(egrad.isfinite(), egrad, zero(egrad)))

@@ -130,6 +130,29 @@ def test_plus_infinity_and_nan_poison_their_token_only():
         assert bool(loss[2:].isfinite().all()) and bool(got[2:].isfinite().all())
 
 
+@pytest.mark.parametrize("t,v", [(3, 40000), (130, 40000), (130, 700), (3, 5)])
+@pytest.mark.parametrize("size", [1e-30, 1e4, 1e8, 3e9, 1e12, 1e37, 3e38])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_logits_of_any_size(t, v, size, dt):
+    """Far beyond where 2^(x log2 e - c) is a float32 number, and with ties at the top."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(v + t)
+    x = ((2 * torch.rand((t, v), device="cuda", generator=g) - 1) * size).to(T[dt])
+    x[0, -1] = x[0, 0] = x[0].max()
+    y = torch.randint(0, v, (t,), device="cuda", generator=g)
+    y[0] = v - 1
+    grads = [c[0] for c in cut(torch.zeros_like(x), 3 if v > 5 else 2)]
+    loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+    print(f"[case] xent size={size} t={t} v={v} {dt}", flush=True)
+    B.ra_cross_entropy([c[0] for c in cut(x, len(grads))], y, loss, lse, grads=grads)
+    wl, wz, wg, el, ez, eg = R.xent(x, y, v, None, 1.0)
+    big = torch.finfo(torch.float32).max
+    wl = torch.where(wl > big * (1 + 2.0 ** -25), math.inf, wl)       # a difference float32 does not hold
+    R.check(loss, wl, el + R.U * wl.abs(), "loss")
+    R.check(lse, wz, ez, "lse")
+    R.check(torch.cat(grads, 1), wg, R.rounded(wg, eg, T[dt]), "grad")
+
+
 def test_gradient_against_differences():
     require_gpu()
     t, v = 6, 1003
