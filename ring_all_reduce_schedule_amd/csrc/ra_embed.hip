@@ -225,8 +225,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(EmbedBwdArgs a, Sor
 
 // ---------------------------------------------------------------- adding up the runs
 
-// Sorted positions of one stretch, and rows that one workgroup clears.
-constexpr int kRun = 16, kClear = 8;
+// Sorted positions of one stretch, and the most rows that one workgroup clears.
+constexpr int kRun = 16, kClearMost = 256;
 
 // Two launches after the sort's: the stretches' runs, together with zeros for the
 // rows that have no tokens; then the runs that cross stretches.
@@ -237,6 +237,7 @@ struct RunArgs {
   int32_t sorted;     // positions
   int32_t stretches;
   int32_t columns;    // workgroups to a stretch, of 256 units
+  int32_t clear;      // rows that a workgroup clears, at most kClearMost
 };
 
 template <int TT, int AC>
@@ -271,31 +272,35 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int key) {
   return lo;
 }
 
-// Zeros for those of rows [v0, v0 + kClear) that no token has.  A workgroup to
-// eight rows (131,072 rows of 16 KiB, with the runs of 16384 tokens beside them,
-// 400 us; four rows 415).  A bit for each row, set by a launch before, in place of the
-// search here, and a workgroup to a row took 443 us for the zeros alone: a
-// workgroup that waits for one load has to write more than a few KiB.
+// Zeros for those of rows [v0, v0 + g.clear) that no token has.  A workgroup that
+// waits for a search has to write more than a few KiB: it has eight rows of 16 KiB
+// (131,072 of them, with the runs of 16384 tokens beside them, 400 us; four rows
+// 415; a bit for each row, set by a launch before, in place of the search, and a
+// workgroup to a row 443 for the zeros alone), and more of shorter ones (70,144 rows
+// of 768 bytes: 16 us with 68 to a workgroup, 38 with eight).
 template <int TT, int AC>
 __device__ __forceinline__ void clear_rows(const EmbedBwdArgs& a, const RunArgs& g, int v0) {
-  __shared__ int taken[kClear];
-  const int v1 = min(a.vocab, v0 + kClear);
-  if (threadIdx.x < kClear) taken[threadIdx.x] = 0;
+  __shared__ int taken[kClearMost];
+  const int v1 = min(a.vocab, v0 + g.clear);
+  taken[threadIdx.x] = 0;
   __syncthreads();
   const int from = lower_bound(g.keys, g.sorted, v0), to = lower_bound(g.keys, g.sorted, v1);
   for (int i = from + (int)threadIdx.x; i < to; i += 256) taken[g.keys[i] - v0] = 1;
   __syncthreads();
-  for (int v = v0; v < v1; ++v) {
+  // 16 bytes to a thread where rows are aligned, else a unit: neighbouring threads
+  // next to each other, and several short rows at a time
+  constexpr int kV = AC != 0 ? 16 / ElemSize<TT>::value : kU;
+  const int vecs = (a.hidden + kV - 1) / kV;
+  const int sub = vecs < 256 ? (int)threadIdx.x / vecs : 0, subs = vecs < 256 ? 256 / vecs : 1;
+  if (sub >= subs) return;
+  for (int v = v0 + sub; v < v1; v += subs) {
     if (taken[v - v0]) continue;
     const int r = piece_of(a.cut, v);
     const int64_t row = (int64_t)(v - piece_lo(a.cut, r)) * a.hidden;
-    if constexpr (AC != 0) {
-      // 16 bytes a lane, next to each other
-      u32x4* at = reinterpret_cast<u32x4*>(static_cast<char*>(a.table.b[r]) + row * ElemSize<TT>::value);
-      for (int j = threadIdx.x; j < a.hidden / (16 / ElemSize<TT>::value); j += 256) at[j] = u32x4{0, 0, 0, 0};
-    } else {
-      for (int j = threadIdx.x; j * kU < a.hidden; j += 256)
-        store_cut<TT, AC>(a.table.b[r], row, unit_cut<AC>(j, a.hidden), Unit<TT>{});
+    u32x4* at = reinterpret_cast<u32x4*>(static_cast<char*>(a.table.b[r]) + row * ElemSize<TT>::value);
+    for (int j = (int)threadIdx.x - sub * vecs; j < vecs; j += 256) {
+      if constexpr (AC != 0) at[j] = u32x4{0, 0, 0, 0};
+      else store_cut<TT, AC>(a.table.b[r], row, unit_cut<AC>(j, a.hidden), Unit<TT>{});
     }
   }
 }
@@ -304,7 +309,7 @@ template <int DT, int TT, int AC>
 __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
   const int stretch = blockIdx.x / g.columns, j = blockIdx.x % g.columns * 256 + threadIdx.x;
   if (stretch >= g.stretches) {
-    clear_rows<TT, AC>(a, g, ((int)blockIdx.x - g.stretches * g.columns) * kClear);
+    clear_rows<TT, AC>(a, g, ((int)blockIdx.x - g.stretches * g.columns) * g.clear);
     return;
   }
   const int lo = stretch * kRun, n = min(g.sorted - lo, kRun), lane = threadIdx.x % 64;
@@ -434,16 +439,23 @@ int64_t embed_bwd_words(int64_t tokens, int hidden) {
 
 static int columns_of(int hidden, int units) { return (hidden + units * kU - 1) / (units * kU); }
 
+// Rows to a workgroup that clears: 65,536 elements of them, but 1024 workgroups if there
+// are rows for that, and eight at least.
+static int clear_of(int vocab, int hidden) {
+  const int most = std::min({kClearMost, 65536 / hidden, std::max(vocab / 1024, 8)});
+  return std::max(most, 8);
+}
+
 // One dispatch counts threads in 32 bits.
 bool embed_bwd_fits(int64_t tokens, int vocab, int hidden) {
   return tokens < (1ll << 31) - kLargeTile &&
-         stretches_of(tokens) * columns_of(hidden, kJoinUnits) + (vocab + kClear - 1) / kClear <=
+         stretches_of(tokens) * columns_of(hidden, kJoinUnits) + (vocab + 7) / 8 <=
              0xFFFFFFFFll / 256;
 }
 
 template <int DT, int TT>
 static hipError_t runs_go(const EmbedBwdArgs& a, const RunArgs& g, bool al, hipStream_t s) {
-  const int clears = a.accumulate ? 0 : (a.vocab + kClear - 1) / kClear;
+  const int clears = a.accumulate ? 0 : (a.vocab + g.clear - 1) / g.clear;
   const unsigned grid = (unsigned)(g.stretches * g.columns + clears);
   if (grid == 0) return hipSuccess;
   if (al) k_embed_runs<DT, TT, kAlignedRows><<<grid, 256, 0, s>>>(a, g);
@@ -495,6 +507,7 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
   g.sorted = (int32_t)n;
   g.stretches = (int32_t)stretches_of(n);
   g.columns = columns_of(a.hidden, 256);
+  g.clear = clear_of(a.vocab, a.hidden);
   if (dtype == 1) return runs_go<1, 1>(a, g, al, s);
   if (dtype == 2) return table_dtype == 1 ? runs_go<2, 1>(a, g, al, s) : runs_go<2, 2>(a, g, al, s);
   return table_dtype == 1 ? runs_go<3, 1>(a, g, al, s) : runs_go<3, 3>(a, g, al, s);

@@ -64,6 +64,7 @@ BACKWARD = [
     (64, 4096, 33, 24, "f32", "f32", "zipf", 0), (8, 4097, 300, 16, "bf16", "f32", "zipf", 0), (8, 5000, 70000, 8, "f16", "f32", "any", 0),
     (8, 20000, 600, 40, "bf16", "bf16", "zipf", 0), (5, 12345, 300_001, 9, "f32", "f32", "far", 0), (1, 9000, 2, 17, "bf16", "f32", "same", 0),
     (8, 70000, 131072, 16, "bf16", "f32", "zipf", 0), (3, 8192, 511, 8, "f32", "f32", "any", 0), (3, 8193, 512, 8, "f32", "f32", "far", 0),
+    (9, 3, 70144, 192, "f32", "f32", "any", 0), (2, 21, 39548, 191, "f16", "f16", "far", 1), (4, 9, 300_000, 3, "bf16", "f32", "any", 0),
 ]
 
 
