@@ -10,7 +10,8 @@
  *   [Derive]    "Derive the cost of a ring all-reduce" (aiinfrainterviews.com)
  *   [Deepinsea] "AllReduce 与 Ring 通信算法详解" (deepinsea.top)
  *
- * Conventions shared by every entry point
+ * Conventions shared by the all-reduce entry points (the row operators at the end
+ * of this file state their own)
  * ---------------------------------------
  *  bufs    host array of p device pointers, one buffer per rank.  The array is
  *          read during the call only and never retained.  Every buffer holds n

@@ -197,7 +197,8 @@ def _marshal_list(tensors):
 class RankBuffers:
     """p rank tensors checked and marshalled once, for repeated calls.
 
-    Every entry point accepts one in place of a list of tensors.  A list is
+    Every entry point accepts one in place of a list of tensors (the row operators
+    save its checks for the buffers they fold, and check their other lists anew).  A list is
     checked and turned into a pointer table on every call, which costs about
     0.8 us of host time per rank (about 50 us at p = 64, more than a fused
     all-reduce of 1 MiB per rank takes on the GPU); this object does it once.
@@ -406,6 +407,11 @@ def _arg(what, t, numel, dtype, dev):
     return t.data_ptr()
 
 
+def _list(tensors):
+    """The tensors of a list or a RankBuffers."""
+    return tensors.tensors if isinstance(tensors, RankBuffers) else tensors
+
+
 def _first(what, tensors):
     if len(tensors) == 0:
         raise ValueError(f"need at least one tensor in {what}")
@@ -495,7 +501,7 @@ def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=No
     scales: as many float32 tensors, one value a token or a group of columns."""
     torch = _torch()
     b0, table, at, p, code, tokens, hidden, dev = _rows(bufs, weight)
-    n, dtype, f32 = tokens * hidden, b0.dtype, torch.float32
+    n, dtype, f32, outs = tokens * hidden, b0.dtype, torch.float32, _list(outs)
     out_type = _first("outs", outs).dtype
     f8 = out_type is torch.float8_e4m3fn
     out_table = _table("outs", outs, n, out_type, dev)
@@ -521,7 +527,7 @@ def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), 
     output; see include/ra.h."""
     torch = _torch()
     d0, table, at, p, code, tokens, hidden, dev = _rows(dys, weight)
-    n, f32 = tokens * hidden, torch.float32
+    n, f32, dxs = tokens * hidden, torch.float32, _list(dxs)
     dx_table = _table("dxs", dxs, n, d0.dtype, dev)
     keep, wp, wn = None, None, 0
     if dweight is not None:
@@ -545,6 +551,7 @@ def _index(what, t, tokens, dev):
 
 def _xent_args(logits, targets, grads):
     """(first tensor, tables to keep, targets' arguments, tokens, vocab, device index)."""
+    logits, grads = _list(logits), _list(grads)
     x0 = _first("logits", logits)
     tokens, dev = targets.numel(), x0.get_device()
     table, vocab = _cut_table("logits", logits, 1, tokens)
@@ -593,6 +600,7 @@ def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
     """outs = scale times the rows of a table cut over the ranks; see include/ra.h.
 
     tables: a list of [rows of the rank, hidden] tensors."""
+    tables, outs = _list(tables), _list(outs)
     t0 = _first("tables", tables)
     hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
     table, vocab = _cut_table("tables", tables, 0, hidden)
@@ -606,6 +614,7 @@ def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
 def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspace=None, stream=None):
     """dtables = (or with accumulate +=) scale times the sums of dy's rows by token; see
     include/ra.h."""
+    dtables = _list(dtables)
     t0 = _first("dtables", dtables)
     hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
     table, vocab = _cut_table("dtables", dtables, 0, hidden)

@@ -275,6 +275,32 @@ def test_binding_refuses_what_does_not_fit():
     torch.cuda.synchronize()
 
 
+def test_rank_buffers_in_place_of_lists():
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(10)
+
+    def n(*shape):
+        return torch.randn(shape, device="cuda", generator=g)
+    bufs, w, ids = [n(6, 24) for _ in range(3)], n(24), torch.tensor([0, 5, 5, 2, -1, 8], device="cuda")
+    logits, tables, h, r = [n(6, 4) for _ in range(3)], [n(3, 24) for _ in range(3)], n(6, 24), n(6).abs()
+
+    def run(wrap):
+        out = [[torch.empty(6, 24, device="cuda") for _ in range(3)] for _ in range(3)]
+        grads, dt = [torch.empty(6, 4, device="cuda") for _ in range(3)], [torch.empty(3, 24, device="cuda") for _ in range(3)]
+        dh = torch.empty(6, 24, device="cuda")
+        B.ra_allreduce_rmsnorm(wrap(bufs), w, 1e-5, wrap(out[0]))
+        B.ra_allreduce_rmsnorm_backward(wrap(bufs), h, r, w, dh, dxs=wrap(out[1]))
+        B.ra_embedding(wrap(tables), ids, wrap(out[2]))
+        B.ra_embedding_backward(h, ids, wrap(dt))
+        B.ra_cross_entropy(wrap(logits), ids, lse=r.clone(), grads=wrap(grads))
+        lse = torch.empty(6, device="cuda")
+        B.ra_cross_entropy(wrap(logits), ids, lse=lse)
+        again = [torch.empty(6, 4, device="cuda") for _ in range(3)]
+        B.ra_cross_entropy_backward(wrap(logits), ids, lse, wrap(again))
+        return out[0] + out[1] + out[2] + grads + dt + again + [dh]
+    assert all(torch.equal(a, b) for a, b in zip(run(list), run(B.RankBuffers)))
+
+
 def test_a_sum_and_its_norm_agree_with_the_all_reduce():
     """Integers small enough that every order and rounding gives the same sum: the norm's h is
     what ra_allreduce leaves."""
