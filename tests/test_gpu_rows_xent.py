@@ -38,7 +38,8 @@ CASES = [
     (4, 514, 33000, 33000, "f32", 0), (8, 512, 65536, 65536, "bf16", 0), (3, 513, 70001, 70000, "bf16", 0),
     (8, 96, 40000, 39990, "bf16", 0), (8, 97, 40000, 39990, "f16", 0), (3, 130, 70001, 70000, "bf16", 0),
     (5, 40, 66001, 66001, "f32", 1), (8, 300, 128000, 128000, "bf16", 0), (2, 61, 16390, 16390, "f16", 0),
-    (8, 512, 131072, 131072, "bf16", 0), (1, 512, 151_937, 151_900, "f16", 0), (2, 512, 140_000, 140_000, "f32", 0),
+    (3, 4, 1_000_003, 1_000_000, "bf16", 0), (3, 97, 1_000_003, 1_000_003, "f16", 0), (2, 3, 1 << 24, 1 << 24, "bf16", 0),
+    (7, 98, 1 << 20, 1 << 20, "f32", 0), (8, 512, 131072, 131072, "bf16", 0), (1, 512, 151_937, 151_900, "f16", 0), (2, 512, 140_000, 140_000, "f32", 0),
 ]
 
 
