@@ -697,6 +697,7 @@ int64_t xent_words(int64_t tokens, int splits) { return splits > 1 ? tokens * (k
 //               8192: 1 token 8.1 / 9.3, 192 9.9 / 10.0
 int xent_splits(int64_t tokens, int vocab, int p, bool grad) {
   const int chunks = total_chunks(vocab, p);
+  if (tokens < 1) return 1;      // the workspace of an empty batch is asked for, too
   if (vocab / p < kU || (grad ? tokens > 96 : chunks <= 64 || tokens > chunks / 2)) return 1;
   // two chunks at least for each wave of a row's workgroups
   const int64_t most = std::min<int64_t>(64, chunks / (2 * kSplitWaves));
