@@ -350,8 +350,8 @@ int ra_cross_entropy(void* const* logits, int p, int64_t tokens, int64_t vocab, 
                      hipStream_t stream) {
   int rc = check_xent(logits, p, tokens, vocab, valid, dtype, target_dtype);
   if (rc != RA_OK) return rc;
+  if (tokens == 0) return RA_OK;   // before the next line: an empty array's address may be NULL
   if (!loss && !lse && !grads) return fail(RA_ERR_INVALID_ARG, "loss, lse and grads are all NULL");
-  if (tokens == 0) return RA_OK;
   Arrays all;
   ra::XentArgs a;
   std::memset(&a, 0, sizeof a);

@@ -5,7 +5,9 @@ import sys
 
 import pytest
 
+from ring_all_reduce_schedule_amd import binding as B
 from tests.conftest import ROOT
+from tests.test_rows_cpu import XENT, call
 
 
 def in_child(code):
@@ -19,3 +21,9 @@ def test_cross_entropy_workspace_of_an_empty_batch(vocab, p):
     """Few tokens of a large vocabulary share their rows among workgroups: none are as many as 1024 / 0."""
     res = in_child(f"assert B.ra_cross_entropy_workspace(0, {vocab}, {p}) == 0")
     assert res.returncode == 0, (res.returncode, res.stderr)
+
+
+def test_cross_entropy_of_an_empty_batch_has_empty_outputs():
+    """An empty tensor's address is NULL: with no rows, that is no missing array."""
+    assert call("ra_cross_entropy", XENT, tokens=0, loss=None, lse=None, grads=None, targets=None) == B.RA_OK
+    assert call("ra_cross_entropy", XENT, tokens=0, loss=None, lse=None, grads=None, vocab=0) == B.RA_ERR_INVALID_ARG
