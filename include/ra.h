@@ -543,6 +543,10 @@ int ra_embedding(const void* const* tables, int p, int64_t vocab, int64_t hidden
  *            0 too).  1: the rows that tokens have are added to, others left alone.
  *   ids outside 0..vocab-1 have no row and are ignored
  *   workspace  ra_embedding_backward_workspace bytes
+ * One call takes fewer than 2^31 - 4096 tokens, and at most
+ *     ceil(tokens / 16) * ceil(hidden / 512) + ceil(vocab / 8)  <=  2^24 - 1
+ * (else RA_ERR_UNSUPPORTED, from the workspace call too): some 200 million tokens of 512
+ * columns, or 14 million of 8192.  Larger batches go in parts, with accumulate.
  */
 int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dtype,
                           const void* ids, int id_dtype, float scale, void* const* dtables, int p,

@@ -157,6 +157,14 @@ int64_t xent_bytes(int64_t tokens, int64_t vocab, int p, bool grad) {
   return ra::xent_words(tokens, ra::xent_splits(tokens, (int)vocab, p, grad)) * (int64_t)sizeof(float);
 }
 
+// The sizes that one call of the embedding's gradient takes.  The workspace call asks this
+// too: beyond them its size would not be one, and pass 64 bits in the end.
+int check_embed_bwd(int64_t tokens, int64_t vocab, int64_t hidden) {
+  if (ra::embed_bwd_fits(tokens, (int)vocab, (int)hidden)) return RA_OK;
+  return fail(RA_ERR_UNSUPPORTED, "tokens = %lld of %lld columns: too many for one call", (long long)tokens,
+              (long long)hidden);
+}
+
 // Logits and gradients of a cross entropy, and what both directions need of them.
 int check_xent(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype, int target_dtype) {
   int rc = check_ranks(p);
@@ -438,6 +446,7 @@ int ra_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidde
   if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
   int rc = check_rows(tokens, hidden, ra::kEmbedMaxHidden, "hidden");
   if (rc == RA_OK) rc = check_rows(0, vocab, ra::kXentMaxVocab, "vocab");
+  if (rc == RA_OK) rc = check_embed_bwd(tokens, vocab, hidden);
   if (rc == RA_OK) *bytes = ra::embed_bwd_words(tokens, (int)hidden) * 4;
   return rc;
 }
@@ -452,9 +461,8 @@ int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dt
   if (rc == RA_OK) rc = check_rows(tokens, hidden, ra::kEmbedMaxHidden, "hidden");
   if (rc == RA_OK) rc = check_rows(0, vocab, ra::kXentMaxVocab, "vocab");
   if (rc != RA_OK) return rc;
-  if (!ra::embed_bwd_fits(tokens, (int)vocab, (int)hidden))
-    return fail(RA_ERR_UNSUPPORTED, "tokens = %lld of %lld columns: too many for one call", (long long)tokens,
-                (long long)hidden);
+  rc = check_embed_bwd(tokens, vocab, hidden);
+  if (rc != RA_OK) return rc;
   if (tokens == 0 && accumulate) return RA_OK;
   const int e = ra::elem_bytes(dtype), et = ra::elem_bytes(dtable_dtype), ei = ra::elem_bytes(id_dtype);
   const int64_t need = ra::embed_bwd_words(tokens, (int)hidden) * 4;
