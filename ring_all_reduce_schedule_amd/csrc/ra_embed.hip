@@ -318,8 +318,12 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
   const int near = lo - 1 + lane;
   const int keys = lane < n + 2 && near >= 0 && near < g.sorted ? g.keys[near] : -1;
   const int places = lane < n ? g.pos[lo + lane] : 0;
-  if (j * kU >= a.hidden) return;
-  const Cut u = unit_cut<AC>(j, a.hidden);
+  // A wave stays whole as long as any lane has a unit: keys and places are read from
+  // lanes, and what a lane that has left holds may be anything.  (All of them read into
+  // scalars before lanes leave: 14 scalars of the odd-row kernels do not fit.)
+  if ((j - lane) * kU >= a.hidden) return;
+  const bool in = j * kU < a.hidden;
+  const Cut u = unit_cut<AC>(in ? j : (a.hidden - 1) / kU, a.hidden);
   // all the stretch's rows at once
   Unit<DT> rows[kRun];
 #pragma unroll
@@ -337,8 +341,8 @@ __global__ __launch_bounds__(256) void k_embed_runs(EmbedBwdArgs a, RunArgs g) {
       if (k + 1 == n || next != key) {
         if (open || next == key) {
           const int64_t slot = ((int64_t)stretch * 2 + (open ? 0 : 1)) * a.hidden;
-          store_cut<1, AC>(g.part, slot, u, unit_make<1>(sum));
-        } else {
+          if (in) store_cut<1, AC>(g.part, slot, u, unit_make<1>(sum));
+        } else if (in) {
           put_row<TT, AC>(a, key, u, sum);
         }
         open = false;
