@@ -157,8 +157,10 @@ def _torch():
 
 
 def dtype_code(t):
-    _torch()
     code = _codes.get(t.dtype)
+    if code is None:
+        _torch()
+        code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype} "
                         "(int32, int64, float16, bfloat16, float32, float64)")
@@ -207,11 +209,12 @@ class RankBuffers:
     ``set_``) meanwhile: the table holds the addresses they had when it was made,
     and a call raises if the first rank's address or length has changed."""
 
-    __slots__ = ("tensors", "ptrs", "p", "n", "dtype", "device", "_first")
+    __slots__ = ("tensors", "ptrs", "p", "n", "dtype", "device", "shapes", "_first")
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
         self.ptrs, self.p, self.n, self.dtype, self.device = _marshal_list(self.tensors)
+        self.shapes = tuple({t.shape for t in self.tensors})
         self._first = (self.tensors[0].data_ptr(), self.n)
 
     def __len__(self):
@@ -346,19 +349,27 @@ def ra_stream_copy_resident(dst, src, grid=0, stream=None):
 
 
 # ---------------------------------------------------------------- row operators
-# Tensors are [tokens, hidden], or have those as their last dimensions flattened:
-# only the number of elements and the last dimension count.  The calls write into
-# the tensors they are given and return None; scratch memory is taken from torch's
-# allocator on the call's stream, so that a captured graph owns its own.
+# Arrays of rows are tensors [..., hidden] whose other dimensions together are the
+# tokens, or flat ones, whose rows lie one behind the other; of values for each token
+# only the number counts.  The calls write into the tensors they are given and return
+# None; scratch memory is taken from torch's allocator on the call's stream, so that a
+# captured graph owns its own.
 
-def _refuse(what, t, numel, dtype, dev):
+def _refuse(what, t, numel, dtype, dev, hidden=None):
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the device of the other tensors")
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
     if t.numel() != numel:
         raise ValueError(f"{what} has {t.numel()} elements, expected {numel}")
+    if hidden is not None and _other_rows(t.shape, hidden):
+        raise ValueError(f"{what} of shape {tuple(t.shape)} are no rows of {hidden}")
     raise ValueError(f"{what} must be contiguous")
+
+
+def _other_rows(shape, hidden):
+    """Whether a tensor of this shape has rows, but not of `hidden` elements."""
+    return len(shape) > 1 and shape[-1] != hidden
 
 
 # Small calls take less time on the GPU than these checks do on the host, so the
@@ -371,6 +382,18 @@ def _table(what, tensors, numel, dtype, dev):
                 or not t.is_contiguous()):
             _refuse(what, t, numel, dtype, dev)
     return array.array("Q", [t.data_ptr() for t in tensors])
+
+
+def _row_table(what, tensors, shape, numel, hidden, dtype, dev):
+    """The same for arrays of rows; `shape` is one that is `numel` elements in such rows, and
+    the tensors of a call mostly have it."""
+    tensor = _torch().Tensor
+    get_device, is_contiguous = tensor.get_device, tensor.is_contiguous
+    for t in tensors:
+        if (t.dtype is not dtype or get_device(t) != dev or not is_contiguous(t)
+                or t.shape != shape and (t.numel() != numel or _other_rows(t.shape, hidden))):
+            _refuse(what, t, numel, dtype, dev, hidden)
+    return array.array("Q", list(map(tensor.data_ptr, tensors)))
 
 
 def _cut_table(what, tensors, dim, other):
@@ -407,6 +430,16 @@ def _arg(what, t, numel, dtype, dev):
     return t.data_ptr()
 
 
+def _row_arg(what, t, shape, numel, hidden, dtype, dev):
+    """The same for an array of rows."""
+    if t is None:
+        return None
+    if (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+            or t.shape != shape and (t.numel() != numel or _other_rows(t.shape, hidden))):
+        _refuse(what, t, numel, dtype, dev, hidden)
+    return t.data_ptr()
+
+
 def _list(tensors):
     """The tensors of a list or a RankBuffers."""
     return tensors.tensors if isinstance(tensors, RankBuffers) else tensors
@@ -423,14 +456,11 @@ def _first(what, tensors):
 
 def _run_on(dev, stream, function, args):
     """function(*args, stream handle) with the tensors' device current."""
-    torch = _torch()
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    core = _torch_module._C
+    handle = core._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if core._cuda_getDevice() == dev:
         return _check(function(*args, handle))
-    with torch.cuda.device(dev):
+    with _torch_module.cuda.device(dev):
         return _check(function(*args, handle))
 
 
@@ -477,20 +507,23 @@ def ra_embedding_backward_workspace(tokens, vocab, hidden):
 
 
 def _rows(bufs, weight):
-    """(first tensor, pointer table, address, p, dtype code, tokens, hidden, device index)."""
-    torch = _torch()
+    """(first tensor, its shape, pointer table, address, p, dtype code, tokens, hidden, device
+    index)."""
+    hidden = weight.numel()
     if isinstance(bufs, RankBuffers):
-        table, p, n, code, _ = _marshal(bufs)
-        b0, at = bufs.tensors[0], table
+        at, p, n, code, _ = _marshal(bufs)
+        b0, table = bufs.tensors[0], at
+        shape, dev = b0.shape, b0.get_device()
+        others = [s for s in bufs.shapes if _other_rows(s, hidden)]
+        shape = others[0] if others else shape
     else:
         b0 = _first("rank buffers", bufs)
-        n, code = b0.numel(), dtype_code(b0)
-        table = _table("rank buffers", bufs, n, b0.dtype, b0.get_device())
+        code, shape, n, dev = dtype_code(b0), b0.shape, b0.numel(), b0.get_device()
+        table = _row_table("rank buffers", bufs, shape, n, hidden, b0.dtype, dev)
         p, at = len(bufs), _address(table)
-    hidden = weight.numel()
-    if hidden == 0 or n % hidden:
-        raise ValueError(f"rank buffers of {n} elements are no rows of {hidden}")
-    return b0, table, at, p, code, n // hidden, hidden, b0.get_device()
+    if hidden == 0 or n % hidden or len(shape) > 1 and shape[-1] != hidden:
+        raise ValueError(f"rank buffers of shape {tuple(shape)} are no rows of {hidden}")
+    return b0, shape, table, at, p, code, n // hidden, hidden, dev
 
 
 def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=None, scales=None,
@@ -499,24 +532,29 @@ def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=No
 
     bufs, outs: lists of tensors (bufs: or a RankBuffers).  outs of float8_e4m3fn take
     scales: as many float32 tensors, one value a token or a group of columns."""
-    torch = _torch()
-    b0, table, at, p, code, tokens, hidden, dev = _rows(bufs, weight)
+    b0, shape, table, at, p, code, tokens, hidden, dev = _rows(bufs, weight)
+    torch = _torch_module
     n, dtype, f32, outs = tokens * hidden, b0.dtype, torch.float32, _list(outs)
-    out_type = _first("outs", outs).dtype
+    if len(outs) == 0:
+        raise ValueError("need at least one tensor in outs")
+    out_type = outs[0].dtype
     f8 = out_type is torch.float8_e4m3fn
-    out_table = _table("outs", outs, n, out_type, dev)
+    out_table = _row_table("outs", outs, shape, n, hidden, out_type, dev)
     res = residual if residual is not None else residual_out
-    res_code, res_type = (code, None) if res is None else (dtype_code(res), res.dtype)
+    res_type = dtype if res is None else res.dtype
     scale_table = None
     if f8:
         if scales is None or len(scales) != len(outs):
             raise ValueError("8-bit outputs need as many scales")
         groups = -(-hidden // group) if group > 0 else 1
         scale_table = _table("scales", scales, tokens * groups, f32, dev)
-    args = (at, p, tokens, hidden, code, _arg("residual", residual, n, res_type, dev),
-            _arg("residual_out", residual_out, n, res_type, dev), res_code,
+    args = (at, p, tokens, hidden, code,
+            _row_arg("residual", residual, shape, n, hidden, res_type, dev),
+            _row_arg("residual_out", residual_out, shape, n, hidden, res_type, dev),
+            code if res_type is dtype else dtype_code(res),
             _arg("weight", weight, hidden, dtype, dev), eps, _address(out_table), len(out_table),
-            RA_FLOAT8_E4M3 if f8 else dtype_code(outs[0]), _address(scale_table), int(group),
+            RA_FLOAT8_E4M3 if f8 else code if out_type is dtype else dtype_code(outs[0]),
+            _address(scale_table), int(group),
             _arg("rstd", rstd, tokens, f32, dev))
     _run_on(dev, stream, lib().ra_allreduce_rmsnorm, args)
 
@@ -525,17 +563,18 @@ def ra_allreduce_rmsnorm_backward(dys, h, rstd, weight, dh, dh_in=None, dxs=(), 
                                   workspace=None, stream=None):
     """Gradient of ra_allreduce_rmsnorm from the ranks' parts dys of the gradient of its
     output; see include/ra.h."""
-    torch = _torch()
-    d0, table, at, p, code, tokens, hidden, dev = _rows(dys, weight)
-    n, f32, dxs = tokens * hidden, torch.float32, _list(dxs)
-    dx_table = _table("dxs", dxs, n, d0.dtype, dev)
+    d0, shape, table, at, p, code, tokens, hidden, dev = _rows(dys, weight)
+    n, dtype, h_type, f32, dxs = tokens * hidden, d0.dtype, h.dtype, _torch_module.float32, _list(dxs)
+    dx_table = _row_table("dxs", dxs, shape, n, hidden, dtype, dev)
     keep, wp, wn = None, None, 0
     if dweight is not None:
         keep, wp, wn = _workspace(workspace, d0, stream,
                                   lib().ra_allreduce_rmsnorm_backward_workspace, tokens, hidden)
-    args = (at, p, tokens, hidden, code, _arg("h", h, n, h.dtype, dev), dtype_code(h),
-            _arg("rstd", rstd, tokens, f32, dev), _arg("weight", weight, hidden, d0.dtype, dev),
-            _arg("dh_in", dh_in, n, h.dtype, dev), _arg("dh", dh, n, h.dtype, dev),
+    args = (at, p, tokens, hidden, code, _row_arg("h", h, shape, n, hidden, h_type, dev),
+            code if h_type is dtype else dtype_code(h), _arg("rstd", rstd, tokens, f32, dev),
+            _arg("weight", weight, hidden, dtype, dev),
+            _row_arg("dh_in", dh_in, shape, n, hidden, h_type, dev),
+            _row_arg("dh", dh, shape, n, hidden, h_type, dev),
             _address(dx_table), len(dx_table), _arg("dweight", dweight, hidden, f32, dev), wp, wn)
     _run_on(dev, stream, lib().ra_allreduce_rmsnorm_backward, args)
 
@@ -605,7 +644,8 @@ def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
     hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
     table, vocab = _cut_table("tables", tables, 0, hidden)
     _first("outs", outs)
-    out_table = _table("outs", outs, tokens * hidden, t0.dtype, dev)
+    dtype, shape = t0.dtype, (*ids.shape, hidden)
+    out_table = _row_table("outs", outs, shape, tokens * hidden, hidden, dtype, dev)
     args = (_address(table), len(table), vocab, hidden, dtype_code(t0),
             *_index("ids", ids, tokens, dev), tokens, scale, _address(out_table), len(out_table))
     _run_on(dev, stream, lib().ra_embedding, args)
@@ -620,6 +660,7 @@ def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspa
     table, vocab = _cut_table("dtables", dtables, 0, hidden)
     keep, wp, wn = _workspace(workspace, t0, stream, lib().ra_embedding_backward_workspace,
                               tokens, vocab, hidden)
-    args = (_arg("dy", dy, tokens * hidden, dy.dtype, dev), tokens, hidden, dtype_code(dy),
-            *_index("ids", ids, tokens, dev), scale, _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
+    args = (_row_arg("dy", dy, (*ids.shape, hidden), tokens * hidden, hidden, dy.dtype, dev),
+            tokens, hidden, dtype_code(dy), *_index("ids", ids, tokens, dev), scale,
+            _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
     _run_on(dev, stream, lib().ra_embedding_backward, args)

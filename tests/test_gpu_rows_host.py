@@ -1,9 +1,11 @@
-"""The row operators' calls whose arguments the binding has to tell apart: empty batches."""
+"""The row operators' calls whose arguments the binding has to tell apart: empty batches, rows
+of another length."""
 
 import pytest
 import torch
 
 from ring_all_reduce_schedule_amd import binding as B
+from tests import rows_ref as R
 from tests.gpu_util import require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -37,3 +39,61 @@ def test_an_empty_batch(vocab):
     B.ra_allreduce_rmsnorm_backward([none(h)], none(h), empty, w, none(h), dh_in=none(h), dxs=[none(h)], dweight=dw)
     assert bool((dw == 0).all())
     torch.cuda.synchronize()
+
+
+def shaped(*shape, dtype=torch.float32):
+    return torch.ones(shape, dtype=dtype, device="cuda")
+
+
+def test_rows_of_another_length_are_refused():
+    """As many elements, but not in rows of the weight's or the table's length."""
+    require_gpu()
+    w8, r8, ids4 = shaped(8), shaped(8), torch.zeros(4, dtype=torch.int64, device="cuda")
+
+    def norm(bufs, weight=w8, outs=None, **kw):
+        B.ra_allreduce_rmsnorm(bufs, weight, 1e-5, outs or [shaped(8, 8)], **kw)
+
+    def back(dys, h, dh, **kw):
+        B.ra_allreduce_rmsnorm_backward(dys, h, r8, w8, dh, **kw)
+    wide, fit = (lambda: shaped(4, 16)), (lambda: shaped(8, 8))
+    for refused in (lambda: norm([wide()]), lambda: norm([wide(), wide()], outs=[wide()]),
+                    lambda: norm([fit(), wide()]), lambda: norm(B.RankBuffers([wide()])),
+                    lambda: norm(B.RankBuffers([fit(), wide()])), lambda: norm([shaped(4, 1, 16)]),
+                    lambda: norm([fit()], outs=[wide()]), lambda: norm([fit()], outs=[fit(), wide()]),
+                    lambda: norm([fit(), fit()], outs=B.RankBuffers([wide(), wide()])),
+                    lambda: norm([fit()], residual=wide()), lambda: norm([fit()], residual_out=wide()),
+                    lambda: norm([shaped(64)], outs=[wide()]),
+                    lambda: back([wide()], fit(), fit()), lambda: back([fit()], wide(), fit()),
+                    lambda: back([fit()], fit(), wide()), lambda: back([fit()], fit(), fit(), dh_in=wide()),
+                    lambda: back([fit()], fit(), fit(), dxs=[wide()]),
+                    lambda: B.ra_embedding([shaped(5, 8)], ids4, [shaped(2, 16)]),
+                    lambda: B.ra_embedding([shaped(3, 8), shaped(2, 8)], ids4, [shaped(4, 8), shaped(2, 16)]),
+                    lambda: B.ra_embedding_backward(shaped(2, 16), ids4, [shaped(5, 8)])):
+        with pytest.raises(ValueError, match="rows of 8"):
+            refused()
+    torch.cuda.synchronize()
+
+
+def test_rows_with_several_leading_dimensions_and_flat_ones():
+    """What counts is the last dimension: [2, 4, 8] is [8, 8], and a flat array has its rows one
+    behind the other."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, res, w = [torch.randn((2, 8, 8), device="cuda", generator=g) for _ in range(2)] + [shaped(8)]
+    want, wide = shaped(8, 8), shaped(8, 8)
+    B.ra_allreduce_rmsnorm(list(x.unbind(0)), w, 1e-5, [want], residual=res[0], residual_out=wide)
+    for shape in ((8, 8), (2, 4, 8), (8, 1, 8), (64,)):
+        y, h = shaped(*shape), shaped(*shape)
+        bufs = [b.view(shape) for b in x.unbind(0)]
+        B.ra_allreduce_rmsnorm(bufs, w, 1e-5, [y], residual=res[0].view(shape), residual_out=h)
+        assert torch.equal(y.view(8, 8), want) and torch.equal(h.view(8, 8), wide)
+        y.fill_(0)
+        B.ra_allreduce_rmsnorm(B.RankBuffers([bufs[0], bufs[1].view(8, 8)]), w, 1e-5, [y], residual=res[0])
+        assert torch.equal(y.view(8, 8), want)
+        ids = torch.tensor([0, 3, 3, 1, 4, 2, 0, 1], device="cuda")
+        table, rows, d = torch.randn((5, 8), device="cuda", generator=g), shaped(*shape), shaped(5, 8)
+        B.ra_embedding([table], ids, [rows])
+        assert torch.equal(rows.view(8, 8), table[ids])
+        B.ra_embedding_backward(rows, ids, [d])
+        want_d, err, _ = R.embedding_backward(rows.view(8, 8), ids, 5, 1.0, None)
+        R.check(d, want_d, R.rounded(want_d, err, torch.float32), "dtable")
