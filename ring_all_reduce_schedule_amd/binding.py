@@ -174,7 +174,14 @@ def _stream_handle(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _marshal_list(tensors):
+def _buffer_code(t):
+    """dtype_code, or that of 8-bit outputs."""
+    if t.dtype is _torch().float8_e4m3fn:
+        return RA_FLOAT8_E4M3
+    return dtype_code(t)
+
+
+def _marshal_list(tensors, code_of=dtype_code):
     """(pointer array, p, n, dtype code, device) for a sequence of rank tensors,
     checked: same dtype, length and device, contiguous, on a GPU.  The pointer
     array is a ctypes view of an array.array, which is several times cheaper to
@@ -190,7 +197,7 @@ def _marshal_list(tensors):
             raise ValueError("rank buffers must share dtype, length and device")
         if not t.is_contiguous():
             raise ValueError("rank buffers must be contiguous")
-    code = dtype_code(t0)
+    code = code_of(t0)
     table = array.array("Q", [t.data_ptr() for t in tensors])
     ptrs = (ctypes.c_void_p * len(tensors)).from_buffer(table)
     return ptrs, len(tensors), n, code, t0.device
@@ -199,9 +206,10 @@ def _marshal_list(tensors):
 class RankBuffers:
     """p rank tensors checked and marshalled once, for repeated calls.
 
-    Every entry point accepts one in place of a list of tensors (the row operators
-    save its checks for the buffers they fold, and check their other lists anew).  A list is
-    checked and turned into a pointer table on every call, which costs about
+    Every entry point accepts one in place of a list of tensors that all have the same
+    length (the row operators save its checks for the buffers they fold, and check their
+    other lists anew; their 8-bit outputs may be one, which the other calls refuse).  A
+    list is checked and turned into a pointer table on every call, which costs about
     0.8 us of host time per rank (about 50 us at p = 64, more than a fused
     all-reduce of 1 MiB per rank takes on the GPU); this object does it once.
     It holds references to the tensors, so their memory stays allocated while it
@@ -213,7 +221,8 @@ class RankBuffers:
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        self.ptrs, self.p, self.n, self.dtype, self.device = _marshal_list(self.tensors)
+        marshalled = _marshal_list(self.tensors, _buffer_code)
+        self.ptrs, self.p, self.n, self.dtype, self.device = marshalled
         self.shapes = tuple({t.shape for t in self.tensors})
         self._first = (self.tensors[0].data_ptr(), self.n)
 
@@ -530,8 +539,8 @@ def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=No
                          group=0, rstd=None, stream=None):
     """outs = RMS norm of (residual + the sum of bufs) times weight; see include/ra.h.
 
-    bufs, outs: lists of tensors (bufs: or a RankBuffers).  outs of float8_e4m3fn take
-    scales: as many float32 tensors, one value a token or a group of columns."""
+    bufs, outs: lists of tensors.  outs of float8_e4m3fn take scales: as many float32
+    tensors, one value a token or a group of columns."""
     b0, shape, table, at, p, code, tokens, hidden, dev = _rows(bufs, weight)
     torch = _torch_module
     n, dtype, f32, outs = tokens * hidden, b0.dtype, torch.float32, _list(outs)
@@ -542,7 +551,7 @@ def ra_allreduce_rmsnorm(bufs, weight, eps, outs, residual=None, residual_out=No
     out_table = _row_table("outs", outs, shape, n, hidden, out_type, dev)
     res = residual if residual is not None else residual_out
     res_type = dtype if res is None else res.dtype
-    scale_table = None
+    scale_table, scales = None, _list(scales)
     if f8:
         if scales is None or len(scales) != len(outs):
             raise ValueError("8-bit outputs need as many scales")

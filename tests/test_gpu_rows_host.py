@@ -1,5 +1,5 @@
 """The row operators' calls whose arguments the binding has to tell apart: empty batches, rows
-of another length."""
+of another length, and RankBuffers in place of lists."""
 
 import pytest
 import torch
@@ -97,3 +97,27 @@ def test_rows_with_several_leading_dimensions_and_flat_ones():
         B.ra_embedding_backward(rows, ids, [d])
         want_d, err, _ = R.embedding_backward(rows.view(8, 8), ids, 5, 1.0, None)
         R.check(d, want_d, R.rounded(want_d, err, torch.float32), "dtable")
+
+
+def test_rank_buffers_of_8_bit_outputs_and_their_scales():
+    """A RankBuffers in place of every list of the 8-bit call; other calls refuse such outputs."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(13)
+    bufs, w = [torch.randn((6, 48), device="cuda", generator=g) for _ in range(3)], shaped(48)
+    for group in (0, 32):
+        def run(wrap):
+            outs = [torch.zeros((6, 48), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(3)]
+            scales = [torch.zeros((6, 2 if group else 1), device="cuda") for _ in range(3)]
+            B.ra_allreduce_rmsnorm(wrap(bufs), w, 1e-5, wrap(outs), scales=wrap(scales), group=group)
+            return [o.view(torch.uint8) for o in outs] + scales
+        lists, wrapped = run(list), run(B.RankBuffers)
+        assert all(torch.equal(a, b) for a, b in zip(lists, wrapped)) and bool((wrapped[-1] > 0).all())
+    eight = B.RankBuffers([torch.zeros((6, 48), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(3)])
+    for refused in (lambda: B.ra_allreduce(eight), lambda: B.ra_allreduce_ex(eight, algo="tree"),
+                    lambda: B.ra_reduce_scatter(eight), lambda: B.ra_all_gather(eight),
+                    lambda: B.ra_allreduce_noalloc(eight), lambda: B.ra_allreduce_rmsnorm(eight, w, 1e-5, bufs)):
+        with pytest.raises((B.RaError, TypeError)):
+            refused()
+    with pytest.raises(TypeError):
+        B.ra_allreduce(list(eight.tensors))
+    torch.cuda.synchronize()
