@@ -75,27 +75,31 @@ def c_check_command(out=C_CHECK_BIN):
             "-Wl,-rpath," + os.path.join(rocm, "lib"), "-o", out]
 
 
-HOST_CHECK_SRC = os.path.join(ROOT, "tests", "c", "host_check.cpp")
-HOST_CHECK_BIN = os.path.join(ROOT, "tests", "c", "host_check")
+C_CHECKS = os.path.join(ROOT, "tests", "c")
+HOST_CHECKS = ["host_check", "host_check_rows"]
 
 
-def host_check_commands(objs, out=HOST_CHECK_BIN):
-    """The host side of the ABI under AddressSanitizer: ra_api.cpp again with the
-    sanitizer on its host code only (each -fsanitize= right after -Xarch_host),
-    linked by g++ with the kernels' objects into a program that needs no GPU."""
+def host_check_commands(objs, out=C_CHECKS):
+    """The host side of the ABI under AddressSanitizer: the library's .cpp sources again
+    with the sanitizer on their host code only (each -fsanitize= right after
+    -Xarch_host), linked by g++ with the kernels' objects into programs that need no GPU."""
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
-    api = os.path.join(BUILD, "ra_api_asan.o")
-    main = os.path.join(BUILD, "host_check.o")
-    kernels = [o for o in objs if not o.endswith("ra_api.o")]
-    return [
-        [hipcc(), *FLAGS, "-x", "hip", "-I", INCLUDE, "-I", CSRC, "-Xarch_host", "-fsanitize=address",
-         "-Xarch_host", "-fno-omit-frame-pointer", "-c", os.path.join(CSRC, "ra_api.cpp"), "-o", api],
-        ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address", "-fno-omit-frame-pointer",
-         "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE, "-I", os.path.join(rocm, "include"), "-c",
-         HOST_CHECK_SRC, "-o", main],
-        ["g++", "-fsanitize=address", main, api, *kernels, "-L", os.path.join(rocm, "lib"),
-         "-lamdhip64", "-Wl,-rpath," + os.path.join(rocm, "lib"), "-o", out],
-    ]
+    host = [os.path.splitext(s)[0] for s in SOURCES if s.endswith(".cpp")]
+    checked = [os.path.join(BUILD, h + "_asan.o") for h in host]
+    kernels = [o for o in objs if os.path.splitext(os.path.basename(o))[0] not in host]
+    cmds = [[hipcc(), *FLAGS, "-x", "hip", "-I", INCLUDE, "-I", CSRC, "-Xarch_host", "-fsanitize=address",
+             "-Xarch_host", "-fno-omit-frame-pointer", "-c", os.path.join(CSRC, h + ".cpp"), "-o", o]
+            for h, o in zip(host, checked)]
+    for name in HOST_CHECKS:
+        main = os.path.join(BUILD, name + ".o")
+        cmds += [
+            ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address", "-fno-omit-frame-pointer",
+             "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE, "-I", os.path.join(rocm, "include"), "-c",
+             os.path.join(C_CHECKS, name + ".cpp"), "-o", main],
+            ["g++", "-fsanitize=address", main, *checked, *kernels, "-L", os.path.join(rocm, "lib"),
+             "-lamdhip64", "-Wl,-rpath," + os.path.join(rocm, "lib"), "-o", os.path.join(out, name)],
+        ]
+    return cmds
 
 
 def build(verbose=False):

@@ -77,7 +77,10 @@ class Arrays {
       return fail(RA_ERR_MISALIGNED, "%s%s = %p is not on a boundary of its %d-byte elements", what,
                   index < 0 ? "" : "[]", ptr, elem);
     if (at % fit != 0) aligned_ = false;
-    if (bytes > 0) list_[n_++] = {at, at + (uint64_t)bytes, what, index, write};
+    if (bytes > 0) {
+      if (n_ == kMost) return fail(RA_ERR_UNSUPPORTED, "more than %d arrays in a call", kMost);
+      list_[n_++] = {at, at + (uint64_t)bytes, what, index, write};
+    }
     return RA_OK;
   }
   // ptr may be exactly an array that was added before as read: both are then one, written.
@@ -115,7 +118,9 @@ class Arrays {
     int index;
     bool write;
   };
-  One list_[3 * RA_MAX_RANKS + 16];
+  // Three lists of the ranks' (a norm's buffers, outputs and scales) and single arrays.
+  static constexpr int kMost = 3 * RA_MAX_RANKS + 16;
+  One list_[kMost];
   int n_ = 0;
   bool aligned_ = true;
 };

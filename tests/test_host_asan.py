@@ -1,6 +1,6 @@
 """The C ABI's host code under AddressSanitizer (CPU only).
 
-tests/c/host_check.cpp drives every entry point's argument checks, chunk bounds,
+tests/c/host_check.cpp drives the all-reduce calls' argument checks, chunk bounds,
 overlap detection on 2000 random pointer sets, and algorithm selection, against
 a copy of the library's host code built with -fsanitize=address (build()
 compiles it).  Any heap or stack misuse aborts the program."""
