@@ -143,15 +143,18 @@ def _check(code):
 
 _torch_module = None
 _codes = {}
+_get_device = _is_contiguous = _data_ptr = None    # torch.Tensor's
 
 
 def _torch():
-    global _torch_module
+    global _torch_module, _get_device, _is_contiguous, _data_ptr
     if _torch_module is None:
         import torch
         _codes.update({torch.int32: RA_INT32, torch.float32: RA_FLOAT32,
                        torch.bfloat16: RA_BFLOAT16, torch.float16: RA_FLOAT16,
                        torch.float64: RA_FLOAT64, torch.int64: RA_INT64})
+        _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+        _data_ptr = torch.Tensor.data_ptr
         _torch_module = torch
     return _torch_module
 
@@ -396,13 +399,11 @@ def _table(what, tensors, numel, dtype, dev):
 def _row_table(what, tensors, shape, numel, hidden, dtype, dev):
     """The same for arrays of rows; `shape` is one that is `numel` elements in such rows, and
     the tensors of a call mostly have it."""
-    tensor = _torch().Tensor
-    get_device, is_contiguous = tensor.get_device, tensor.is_contiguous
     for t in tensors:
-        if (t.dtype is not dtype or get_device(t) != dev or not is_contiguous(t)
+        if (t.dtype is not dtype or _get_device(t) != dev or not _is_contiguous(t)
                 or t.shape != shape and (t.numel() != numel or _other_rows(t.shape, hidden))):
             _refuse(what, t, numel, dtype, dev, hidden)
-    return array.array("Q", list(map(tensor.data_ptr, tensors)))
+    return array.array("Q", list(map(_data_ptr, tensors)))
 
 
 def _cut_table(what, tensors, dim, other):
@@ -443,10 +444,10 @@ def _row_arg(what, t, shape, numel, hidden, dtype, dev):
     """The same for an array of rows."""
     if t is None:
         return None
-    if (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()
+    if (t.dtype is not dtype or _get_device(t) != dev or not _is_contiguous(t)
             or t.shape != shape and (t.numel() != numel or _other_rows(t.shape, hidden))):
         _refuse(what, t, numel, dtype, dev, hidden)
-    return t.data_ptr()
+    return _data_ptr(t)
 
 
 def _list(tensors):
@@ -653,9 +654,9 @@ def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
     hidden, dev, tokens = t0.shape[-1], t0.get_device(), ids.numel()
     table, vocab = _cut_table("tables", tables, 0, hidden)
     _first("outs", outs)
-    dtype, shape = t0.dtype, (*ids.shape, hidden)
+    code, dtype, shape = dtype_code(t0), t0.dtype, (*ids.shape, hidden)
     out_table = _row_table("outs", outs, shape, tokens * hidden, hidden, dtype, dev)
-    args = (_address(table), len(table), vocab, hidden, dtype_code(t0),
+    args = (_address(table), len(table), vocab, hidden, code,
             *_index("ids", ids, tokens, dev), tokens, scale, _address(out_table), len(out_table))
     _run_on(dev, stream, lib().ra_embedding, args)
 
