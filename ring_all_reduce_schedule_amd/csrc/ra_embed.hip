@@ -18,9 +18,10 @@
 //
 // Both are bound by writing.  Measured on MI355X (fills reach 6.9 TB/s, copies 6.55):
 //   16384 tokens x 4096 bfloat16 to 8 ranks              213 us, 5.3 TB/s
-//   its gradient, float32, into 131,072 rows              440 us, 5.2 TB/s, of which
+//   its gradient, float32, into 131,072 rows              445 us, 5.1 TB/s, of which
 //     sorting takes 20, joining long runs 12
-//   1003 tokens x 1001 float16 into 5003 rows              20 us in four launches
+//   1003 tokens x 1001 float16 into 5003 rows              20 us in three launches: sort
+//     5.4, runs and zeros 11, joins 3.5
 #include "ra_rows.h"
 
 namespace ra {

@@ -130,8 +130,10 @@ struct NormBwdArgs {
 // Rows longer than this would not stay in the registers of one workgroup.
 constexpr int kNormMaxHidden = 32768;
 
-// Workgroups of the backward pass: two of 1024 threads for each compute unit.  A
-// constant, so that the order in which dw is summed does not depend on the GPU.
+// Workgroups of the backward pass: two for each of 256 compute units.  Those of 1024
+// threads run one after the other, since they take more than the 64 registers that
+// would let two of them share a unit.  A constant, so that the order in which dw is
+// summed does not depend on the GPU.
 constexpr int kNormBwdBlocks = 512;
 
 hipError_t launch_norm(const NormArgs& a, int dtype, int res_dtype, bool f8, int access, hipStream_t s);

@@ -24,7 +24,7 @@
 // both ways).  Measured on MI355X, where a copy of 8 GiB runs at 6.55 TB/s:
 //   4096 x 8192 bfloat16, 8 ranks, 8-bit outputs to all   168 us, 5.6 TB/s
 //   its gradient                                          142 us, 5.7 TB/s
-//   16384 x 8192 bfloat16, one rank                       172 us, 6.2 TB/s
+//   16384 x 8192 bfloat16, one rank, a residual both ways 172 us, 6.2 TB/s
 //   1003 x 5001 float16, 9 ranks, rows on odd addresses    25 us, 5.4 TB/s
 //   1 x 4096 bfloat16, 8 ranks                            3.8 us
 // Asking for 64 registers, to have twice the waves, changed the first two by less
@@ -177,6 +177,8 @@ template <int DT, int RT, int K, int AC>
 __global__ __launch_bounds__(1024) void k_norm_bwd(NormBwdArgs a) {
   const int G = blockDim.x;
   // Four units a thread leave no registers for h: it is read again, from the cache.
+  // All but two of those kernels put 6 to 21 of their 128 registers into scratch even so
+  // (2048 x 32768 bfloat16, one rank: 124 us, where its bytes at a copy's rate take 62).
   constexpr bool kKeep = K <= 2;
   __shared__ float lds_sum[2][16];
   const int tid = threadIdx.x, hidden = a.hidden;

@@ -24,14 +24,17 @@
 // other operations on a logit are kept to a handful.  Measured on MI355X, where a
 // copy of 8 GiB runs at 6.55 TB/s:
 //   8192 x 131072 bfloat16, 8 ranks, with gradient   832 us, 5.2 TB/s
-//   ... the loss alone                               353 us, 6.1 TB/s
-//   ... the gradient alone, from lse                 750 us, 5.7 TB/s
-//   1003 x 50017 float32, 9 ranks, with gradient      98 us, 4.1 TB/s
+//   ... the loss alone                               352 us, 6.1 TB/s
+//   ... the gradient alone, from lse                 760 us, 5.6 TB/s
+//   1003 x 50017 float32, 9 ranks, with gradient      97 us, 4.1 TB/s
 //   4 x 128000 bfloat16, the loss alone              7.0 us in two launches
-// The first took 847 us with the arithmetic left out, the same with the logits in
-// one buffer, and 4% more with half of each row read twice: a row of 256 KiB to a
-// compute unit keeps 256 rows' worth of DRAM pages open where a copy moves through
-// memory in order, and that is what is left.  Rows of 8192 columns reach 5.6 TB/s.
+// The first reads 1.002 times the logits' bytes and writes the gradient's once (HBM
+// counters).  It took 847 us with the arithmetic left out, the same with the logits in
+// one buffer, and 4% more with half of each row read twice; 2^30 logits in rows of 4096
+// to 65536 columns take 768 to 806 us.  So neither bytes nor arithmetic are what is
+// left; which part of the memory system is, no counter has shown.  The float32 kernels
+// with eight units a lane fill the registers (two of 128 go to scratch), and with long
+// rows stay at 4.5-4.7 TB/s.
 #include "ra_rows.h"
 
 namespace ra {
