@@ -425,8 +425,8 @@ int ra_stream_copy_resident(void* dst, const void* src, int64_t bytes, int grid,
  *          then NULL will do).  It is scratch: nothing is kept in it between
  *          calls, and calls that may overlap need one each.  So do HIP graphs
  *          whose replays may overlap.
- *  The calls wait for nothing, allocate nothing and can be captured into HIP
- *  graphs on any stream.  The current device has to be the stream's.
+ *  The calls wait for nothing, allocate no device memory and can be captured into
+ *  HIP graphs on any stream.  The current device has to be the stream's.
  *  tokens == 0 is RA_OK and writes nothing but what a call says.
  */
 
@@ -521,6 +521,50 @@ int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_
                               float grad_scale, hipStream_t stream);
 
 /*
+ * ra_token_logprobs -- what a model answers with, from logits whose vocabulary is cut
+ * over the ranks: log probabilities of given tokens, the entropy, and the `top` best
+ * alternatives, in one reading of the logits:
+ *     ln p_j = scale x_j - lse,   lse = ln sum_j exp(scale x_j)
+ *     logprob = ln p_id,   entropy = - sum_j p_j ln p_j
+ *   logits, valid  as for ra_cross_entropy: columns from `valid` on are no columns here
+ *   scale    > 0 and finite: 1 / temperature
+ *   ids      [tokens] of id_dtype (RA_INT32 or RA_INT64): the given tokens.  Below 0: a
+ *            token without one (logprob 0; the entropy and the alternatives are its row's
+ *            all the same).  From `valid` on: a logprob of NaN.  NULL: none (logprob has to
+ *            be NULL, too).
+ *   logprob, entropy, lse  [tokens] float32; each may be NULL
+ *   top      0..64, at most `valid`
+ *   top_ids, top_logprobs  [tokens][top] of id_dtype, and float32: the columns with the
+ *            largest logits, largest first, and of equal ones the lowest column first; with
+ *            their log probabilities.  Either may be NULL.
+ *   workspace  ra_token_logprobs_workspace bytes
+ * Logits of -inf are masked columns: they come last.  A row all of whose columns are -inf
+ * has lse = -inf, entropy 0 and log probabilities of -inf.  A logit of +inf or NaN makes
+ * its row's numbers NaN; NaN counts as the largest logit.
+ */
+int ra_token_logprobs(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
+                      float scale, const void* ids, int id_dtype, float* logprob, float* entropy,
+                      float* lse, int top, void* top_ids, float* top_logprobs, void* workspace,
+                      int64_t workspace_bytes, hipStream_t stream);
+int ra_token_logprobs_workspace(int64_t tokens, int64_t vocab, int p, int top, int64_t* bytes);
+
+/*
+ * ra_token_logprobs_backward -- the gradient of logprob and entropy:
+ *     dx_j = scale (dlogprob ([j = id] - p_j) - dentropy p_j (ln p_j + entropy))
+ *   lse, entropy   what the forward call left (entropy: needed with dentropy, else ignored)
+ *   dlogprob, dentropy  [tokens] float32: the gradients of the two; NULL: zeros, of one at
+ *            most.  dlogprob needs ids; that of a token whose id is below 0 is taken as 0.
+ *   grads    p arrays like logits; grads[r] may be logits[r]
+ * A token whose two gradients are 0 gets zeros whatever its logits hold, and so does one
+ * all of whose columns are -inf.  An id from `valid` on, or an lse of +inf or NaN, makes
+ * the token's gradient NaN.  Columns from `valid` on get zeros.
+ */
+int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid,
+                               int dtype, float scale, const void* ids, int id_dtype, const float* lse,
+                               const float* entropy, const float* dlogprob, const float* dentropy,
+                               void* const* grads, hipStream_t stream);
+
+/*
  * ra_embedding -- rows of a table whose vocabulary is cut over the ranks, to every
  * rank: y_t = scale * table[id_t].  (Each rank looking up its own rows, zeros for
  * the others, and an all-reduce give the same.)
@@ -553,6 +597,63 @@ int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dt
                           int64_t vocab, int dtable_dtype, int accumulate, void* workspace,
                           int64_t workspace_bytes, hipStream_t stream);
 int ra_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden, int64_t* bytes);
+
+/*
+ * Gradients
+ * ---------
+ * What follows the backward pass: the norm of all gradients together, and clipping by it.
+ * Types, overlap, workspaces and capture as for the row operators.  Squares and their sum
+ * are float64, in an order that the sizes alone decide, so that gradients of any size have
+ * a norm.  Arrays start on a boundary of their elements.
+ *
+ * ra_grad_norm -- norm = scale sqrt(sum of g^2 over every element of n tensors)
+ *   tensors, counts, dtypes  host arrays, read during the call only: addresses, elements
+ *            and types, which may differ from tensor to tensor.  An empty tensor's address
+ *            may be NULL.  At most 2^20 tensors, and 2^44 elements in all.
+ *   scale    > 0 and finite: what the gradients are to be multiplied with (1 / the loss's
+ *            scale, 1 / the number of batches)
+ *   norm     one float32.  n = 0: 0.
+ *   workspace  ra_grad_norm_workspace bytes
+ */
+int ra_grad_norm(const void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n,
+                 float scale, float* norm, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int ra_grad_norm_workspace(int64_t n, int64_t* bytes);
+
+/*
+ * ra_grad_clip -- the gradients scaled so that their norm is at most max_norm:
+ *     c = scale min(1, max_norm / (norm + 1e-6)),   out = g c
+ *   counted   0..n: the first `counted` tensors make the norm, and all n are scaled (a
+ *             parameter that several ranks hold a copy of counts once)
+ *   max_norm  > 0; INFINITY: no clipping, only scale and the norm
+ *   outs, out_dtypes  where the scaled gradients go: arrays like the tensors, of the tensors' type or
+ *             RA_FLOAT32.  outs NULL: in place.  out_dtypes NULL: the tensors' types.
+ *             outs[i] may be tensors[i], where the types are the same.
+ *   norm      the norm before clipping, scale included
+ *   workspace  ra_grad_norm_workspace bytes
+ * c is computed in float64 and rounded to float32.  The products are float32, rounded
+ * once.  With a norm that is not finite c is 0 or NaN: look at norm before the outputs
+ * are used.  Tensors that are scaled in place with c = 1 are not written.
+ */
+int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n,
+                 int64_t counted, float max_norm, float scale, void* const* outs, const int* out_dtypes,
+                 float* norm, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ra_allreduce_clip -- an all-reduce of gradients and ra_grad_clip of its result, to the ranks:
+ *     g = sum_r bufs[r]  (RA_AVG: that divided by p), rounded to `dtype`
+ *     norm = scale sqrt(sum g^2),   c = scale min(1, max_norm / (norm + 1e-6)),   out = g c
+ * The ranks' buffers are added in rank order, 0 first, in float32.
+ *   bufs   p arrays of n elements of `dtype` (n up to 2^44)
+ *   op     RA_SUM or RA_AVG
+ *   outs   n_out (1..p) arrays like bufs; each may be one of bufs
+ *   norm, max_norm, scale  as above
+ *   workspace  ra_allreduce_clip_workspace bytes
+ * n = 0: norm gets 0.
+ */
+int ra_allreduce_clip(void* const* bufs, int p, int64_t n, int dtype, int op, float max_norm, float scale,
+                      void* const* outs, int n_out, float* norm, void* workspace,
+                      int64_t workspace_bytes, hipStream_t stream);
+int ra_allreduce_clip_workspace(int64_t n, int64_t* bytes);
 
 #ifdef __cplusplus
 }

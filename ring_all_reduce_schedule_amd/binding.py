@@ -95,6 +95,17 @@ _SIGNATURES = {
     "ra_cross_entropy_workspace": (_int, [_i64, _i64, _int, ctypes.POINTER(_i64)]),
     "ra_cross_entropy_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _vp, _vp,
                                          _vp, _f32, _vp]),
+    "ra_token_logprobs": (_int, [_vp, _int, _i64, _i64, _i64, _int, _f32, _vp, _int, _vp, _vp, _vp,
+                                 _int, _vp, _vp, _vp, _i64, _vp]),
+    "ra_token_logprobs_workspace": (_int, [_i64, _i64, _int, _int, ctypes.POINTER(_i64)]),
+    "ra_token_logprobs_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _f32, _vp, _int, _vp,
+                                          _vp, _vp, _vp, _vp, _vp]),
+    "ra_grad_norm": (_int, [_vp, _vp, _vp, _i64, _f32, _vp, _vp, _i64, _vp]),
+    "ra_grad_norm_workspace": (_int, [_i64, ctypes.POINTER(_i64)]),
+    "ra_grad_clip": (_int, [_vp, _vp, _vp, _i64, _i64, _f32, _f32, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "ra_allreduce_clip": (_int, [_vp, _int, _i64, _int, _int, _f32, _f32, _vp, _int, _vp, _vp, _i64,
+                                 _vp]),
+    "ra_allreduce_clip_workspace": (_int, [_i64, ctypes.POINTER(_i64)]),
     "ra_embedding": (_int, [_vp, _int, _i64, _i64, _int, _vp, _int, _i64, _f32, _vp, _int, _vp]),
     "ra_embedding_backward": (_int, [_vp, _i64, _i64, _int, _vp, _int, _f32, _vp, _int, _i64, _int,
                                      _int, _vp, _i64, _vp]),
@@ -516,6 +527,28 @@ def ra_embedding_backward_workspace(tokens, vocab, hidden):
     return n.value
 
 
+def ra_token_logprobs_workspace(tokens, vocab, p, top):
+    """Bytes of workspace (host only)."""
+    n = ctypes.c_int64()
+    _check(lib().ra_token_logprobs_workspace(int(tokens), int(vocab), int(p), int(top),
+                                             ctypes.byref(n)))
+    return n.value
+
+
+def ra_grad_norm_workspace(n):
+    """Bytes of workspace for n tensors (host only)."""
+    size = ctypes.c_int64()
+    _check(lib().ra_grad_norm_workspace(int(n), ctypes.byref(size)))
+    return size.value
+
+
+def ra_allreduce_clip_workspace(n):
+    """Bytes of workspace for n elements (host only)."""
+    size = ctypes.c_int64()
+    _check(lib().ra_allreduce_clip_workspace(int(n), ctypes.byref(size)))
+    return size.value
+
+
 def _rows(bufs, weight):
     """(first tensor, its shape, pointer table, address, p, dtype code, tokens, hidden, device
     index)."""
@@ -598,11 +631,12 @@ def _index(what, t, tokens, dev):
     return _arg(what, t, tokens, dtype, dev), _codes[dtype]
 
 
-def _xent_args(logits, targets, grads):
+def _xent_args(logits, targets, grads, what="targets"):
     """(first tensor, tables to keep, targets' arguments, tokens, vocab, device index)."""
     logits, grads = _list(logits), _list(grads)
     x0 = _first("logits", logits)
-    tokens, dev = targets.numel(), x0.get_device()
+    dev = x0.get_device()
+    tokens = x0.shape[0] if targets is None else targets.numel()
     table, vocab = _cut_table("logits", logits, 1, tokens)
     grad_table = None
     if grads is not None:
@@ -614,7 +648,8 @@ def _xent_args(logits, targets, grads):
         grad_table, columns = _cut_table("grads", grads, 1, tokens)
         if columns != vocab:
             raise ValueError("grads must have the logits' shapes")
-    return x0, (table, grad_table), _index("targets", targets, tokens, dev), tokens, vocab, dev
+    goal = (None, RA_INT64) if targets is None else _index(what, targets, tokens, dev)
+    return x0, (table, grad_table), goal, tokens, vocab, dev
 
 
 def ra_cross_entropy(logits, targets, loss=None, lse=None, grads=None, dloss=None, grad_scale=1.0,
@@ -643,6 +678,52 @@ def ra_cross_entropy_backward(logits, targets, lse, grads, dloss=None, grad_scal
             dtype_code(x0), *goal, _arg("lse", lse, tokens, f32, dev), _address(grad_table),
             _arg("dloss", dloss, tokens, f32, dev), grad_scale)
     _run_on(dev, stream, lib().ra_cross_entropy_backward, args)
+
+
+def ra_token_logprobs(logits, ids=None, logprob=None, entropy=None, lse=None, top_ids=None,
+                      top_logprobs=None, scale=1.0, valid=None, workspace=None, stream=None):
+    """Log probabilities of given tokens, entropy and the best alternatives over a vocabulary
+    cut over the ranks; see include/ra.h.
+
+    logits: a list of [tokens, columns of the rank] tensors.  top_ids, top_logprobs:
+    [tokens, k] tensors for the k best columns; top_ids of the type of ids (without ids:
+    int32 or int64)."""
+    torch = _torch()
+    f32 = torch.float32
+    x0, (table, _), (id_at, id_code), tokens, vocab, dev = _xent_args(logits, ids, None, "ids")
+    top, id_type = 0, torch.int64 if ids is None else ids.dtype
+    for t in (top_ids, top_logprobs):
+        if t is None:
+            continue
+        if t.dim() != 2 or t.shape[0] != tokens or top and t.shape[1] != top:
+            raise ValueError(f"top_ids and top_logprobs must be [{tokens}, k], with the same k")
+        top = t.shape[1]
+        if top == 0:
+            raise ValueError("top_ids and top_logprobs must have a column")
+    if top_ids is not None and ids is None:
+        id_type = top_ids.dtype
+        id_code = _index("top_ids", top_ids, tokens * top, dev)[1]
+    keep, wp, wn = _workspace(workspace, x0, stream, lib().ra_token_logprobs_workspace,
+                              tokens, vocab, len(table), top)
+    args = (_address(table), len(table), tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), scale, id_at, id_code, _arg("logprob", logprob, tokens, f32, dev),
+            _arg("entropy", entropy, tokens, f32, dev), _arg("lse", lse, tokens, f32, dev), top,
+            _arg("top_ids", top_ids, tokens * top, id_type, dev),
+            _arg("top_logprobs", top_logprobs, tokens * top, f32, dev), wp, wn)
+    _run_on(dev, stream, lib().ra_token_logprobs, args)
+
+
+def ra_token_logprobs_backward(logits, ids, lse, grads, dlogprob=None, entropy=None, dentropy=None,
+                               scale=1.0, valid=None, stream=None):
+    """The gradient of ra_token_logprobs' logprob and entropy, from the lse and entropy that it
+    left; see include/ra.h.  grads may be the logits themselves."""
+    f32 = _torch().float32
+    x0, (table, grad_table), goal, tokens, vocab, dev = _xent_args(logits, ids, grads, "ids")
+    args = (_address(table), len(table), tokens, vocab, vocab if valid is None else int(valid),
+            dtype_code(x0), scale, *goal, _arg("lse", lse, tokens, f32, dev),
+            _arg("entropy", entropy, tokens, f32, dev), _arg("dlogprob", dlogprob, tokens, f32, dev),
+            _arg("dentropy", dentropy, tokens, f32, dev), _address(grad_table))
+    _run_on(dev, stream, lib().ra_token_logprobs_backward, args)
 
 
 def ra_embedding(tables, ids, outs, scale=1.0, stream=None):
@@ -674,3 +755,90 @@ def ra_embedding_backward(dy, ids, dtables, scale=1.0, accumulate=False, workspa
             tokens, hidden, dtype_code(dy), *_index("ids", ids, tokens, dev), scale,
             _address(table), len(table), vocab, dtype_code(t0), 1 if accumulate else 0, wp, wn)
     _run_on(dev, stream, lib().ra_embedding_backward, args)
+
+
+# ---------------------------------------------------------------- gradients
+
+class TensorList:
+    """Tensors of any sizes and types, checked and marshalled once, for repeated calls of
+    ra_grad_norm and ra_grad_clip, which accept one in place of a list of tensors (checking a
+    list costs about as much host time for 10 tensors as the norm of small ones takes on the
+    GPU).  It holds references to the tensors, which must not be resized or re-pointed
+    meanwhile: the table holds the addresses they had when it was made."""
+
+    __slots__ = ("tensors", "device", "_ptrs", "_counts", "_codes")
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        _torch()
+        dev = _get_device(self.tensors[0]) if self.tensors else -1
+        for t in self.tensors:
+            if not t.is_cuda or _get_device(t) != dev:
+                raise ValueError("tensors must be on one device")
+            if not _is_contiguous(t):
+                raise ValueError("tensors must be contiguous")
+        self.device = dev
+        self._ptrs = array.array("Q", list(map(_data_ptr, self.tensors)))
+        self._counts = array.array("q", [t.numel() for t in self.tensors])
+        self._codes = array.array("i", [dtype_code(t) for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _tensor_list(tensors, norm):
+    """(TensorList, address of norm, device index)."""
+    t = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+    if not norm.is_cuda:
+        raise ValueError("norm must be a device tensor")
+    dev = norm.get_device()
+    if t.device not in (dev, -1):
+        raise ValueError("tensors must be on the device of norm")
+    return t, _arg("norm", norm, 1, _torch().float32, dev), dev
+
+
+def ra_grad_norm(tensors, norm, scale=1.0, workspace=None, stream=None):
+    """norm = scale times the 2-norm over all elements of a list of tensors (or a TensorList);
+    see include/ra.h.  norm: one float32."""
+    t, to, dev = _tensor_list(tensors, norm)
+    keep, wp, wn = _workspace(workspace, norm, stream, lib().ra_grad_norm_workspace, len(t))
+    args = (_address(t._ptrs), _address(t._counts), _address(t._codes), len(t), scale, to, wp, wn)
+    _run_on(dev, stream, lib().ra_grad_norm, args)
+
+
+def ra_grad_clip(tensors, max_norm, norm, outs=None, counted=None, scale=1.0, workspace=None,
+                 stream=None):
+    """Scales tensors (a list or a TensorList; in place, or into outs) so that their norm is at
+    most max_norm; see include/ra.h.  norm, one float32, gets the norm before.  counted: how many
+    of the tensors, from the first on, the norm is of (None: all)."""
+    t, to, dev = _tensor_list(tensors, norm)
+    n, o = len(t), None
+    if outs is not None:
+        o = outs if isinstance(outs, TensorList) else TensorList(outs)
+        if o._counts != t._counts or o.device != t.device:
+            raise ValueError("outs must be tensors of the same sizes, on the same device")
+    keep, wp, wn = _workspace(workspace, norm, stream, lib().ra_grad_norm_workspace, n)
+    args = (_address(t._ptrs), _address(t._counts), _address(t._codes), n,
+            n if counted is None else int(counted), max_norm, scale,
+            None if o is None else _address(o._ptrs), None if o is None else _address(o._codes), to, wp, wn)
+    _run_on(dev, stream, lib().ra_grad_clip, args)
+
+
+def ra_allreduce_clip(bufs, max_norm, norm, outs=None, op="avg", scale=1.0, workspace=None,
+                      stream=None):
+    """The ranks' buffers averaged (op "avg") or added ("sum"), scaled so that their norm is at
+    most max_norm, into outs (None: in place); see include/ra.h.  norm, one float32, gets the
+    norm before."""
+    ptrs, p, n, code, _ = _marshal(bufs)
+    b0 = _list(bufs)[0]
+    dev = b0.get_device()
+    table, n_out = ptrs, p
+    if outs is not None:
+        outs = _list(outs)
+        _first("outs", outs)
+        table, n_out = _table("outs", outs, n, b0.dtype, dev), len(outs)
+    keep, wp, wn = _workspace(workspace, norm, stream, lib().ra_allreduce_clip_workspace, n)
+    args = (ptrs, p, n, code, _op(op), max_norm, scale,
+            ptrs if outs is None else _address(table), n_out,
+            _arg("norm", norm, 1, _torch().float32, dev), wp, wn)
+    _run_on(dev, stream, lib().ra_allreduce_clip, args)

@@ -1,5 +1,5 @@
 // ra_internal.h -- interface between the host API (ra_api.cpp) and the kernel
-// launchers (ra_fused.hip, ra_steps.hip, ra_copy.hip), plus small host helpers.
+// launchers in the .hip files, plus small host helpers.
 // Not installed; the public ABI is include/ra.h.
 #pragma once
 
@@ -147,34 +147,61 @@ struct Pieces {
   int32_t extra;   // n mod p: the first `extra` pieces hold one more
 };
 
-struct XentArgs {
+// Logits whose vocabulary is cut over the ranks.
+struct VocabArgs {
   RankPtrs x, dx;            // the ranks' logits; their gradients (dx.b[0..p) null: not wanted)
+  int64_t tokens, row0;
+  Pieces cut;
+  int32_t p, vocab, valid, splits;
+  // set by vocab_geometry() from cut, p, vocab and valid:
+  int32_t whole;             // chunks of 512 columns in a piece
+  int32_t total;             // chunks of a row: those, and what is left of each piece
+  int32_t full;              // the first chunks, all of whose columns are valid
+  uint32_t magic;            // ceil(2^32 / whole): q / whole = (q magic) >> 32 while q whole < 2^32
+};
+int vocab_chunks(int vocab, int p);
+void vocab_geometry(VocabArgs* a);
+
+struct XentArgs : VocabArgs {
   const void* target;
   const float* dloss;        // or null: 1 for every token
   const float* lse_in;       // backward only
   float* loss;
   float* lse;
   float* part;               // split rows: xent_words() of workspace
-  int64_t tokens, row0;
-  Pieces cut;
-  int32_t p, vocab, valid, target64, splits;
-  // set by xent_geometry() from cut, p, vocab and valid:
-  int32_t whole;             // chunks of 512 columns in a piece
-  int32_t total;             // chunks of a row: those, and what is left of each piece
-  int32_t full;              // the first chunks, all of whose columns are valid
-  uint32_t magic;            // ceil(2^32 / whole): q / whole = (q magic) >> 32 while q whole < 2^32
+  int32_t target64;
   float grad_scale;
 };
 
 // Workgroups that share a row, 1 where a workgroup takes a whole row.
 int xent_splits(int64_t tokens, int vocab, int p, bool grad);
-void xent_geometry(XentArgs* a);
 int64_t xent_words(int64_t tokens, int splits);   // 32-bit words of workspace
 
 // Columns of a vocabulary: chunk numbers times chunks stay below 2^32.
 constexpr int kXentMaxVocab = 1 << 24;
 hipError_t launch_xent(const XentArgs& a, int dtype, bool grad, bool al, hipStream_t s);
 hipError_t launch_xent_bwd(const XentArgs& a, int dtype, bool al, hipStream_t s);
+
+struct LogpArgs : VocabArgs {
+  const void* ids;           // or null: none wanted
+  float* logprob;            // these five or null
+  float* entropy;
+  float* lse;
+  void* top_ids;
+  float* top_logprobs;
+  const float* lse_in;       // backward only, as the next three
+  const float* entropy_in;
+  const float* dlogprob;     // or null
+  const float* dentropy;     // or null
+  float* part;               // split rows: logp_bytes() of workspace
+  int32_t ids64, top;
+  float scale;
+};
+constexpr int kTopMost = 64;   // a lane for each
+int logp_splits(int64_t tokens, int vocab, int p);
+int64_t logp_bytes(int64_t tokens, int splits, int top);
+hipError_t launch_logp(const LogpArgs& a, int dtype, bool al, hipStream_t s);
+hipError_t launch_logp_bwd(const LogpArgs& a, int dtype, bool al, hipStream_t s);
 
 struct EmbedArgs {
   RankPtrs table, out;
@@ -203,6 +230,55 @@ bool embed_bwd_fits(int64_t tokens, int vocab, int hidden);
 // Elements of an embedding's row (columns of workgroups in one dispatch).
 constexpr int kEmbedMaxHidden = 1 << 20;
 hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, bool al, hipStream_t s);
+
+// ---------------------------------------------------------------- gradients
+
+// Tensors of one launch; with the launch's other arguments they stay under 4 KiB.
+constexpr int kBatchTensors = 128;
+struct TensorBatch {
+  const void* in[kBatchTensors];
+  void* out[kBatchTensors];
+  int64_t count[kBatchTensors];
+  uint32_t first[kBatchTensors + 1];    // tiles before each tensor's; from the last one on, all tiles
+  uint8_t type[kBatchTensors];          // of what is read, and 16 times that of what is written
+};
+
+// A caller's list.
+struct TensorListArgs {
+  const void* const* in;
+  void* const* out;          // null: not written
+  const int64_t* counts;
+  const int* types;
+  const int* out_types;      // null: the same
+  int64_t n, counted;        // the first `counted` make the norm
+};
+
+// How a norm and a factor come from the sum of squares.
+struct ClipRule {
+  const double* part;        // `parts` sums
+  const float* factor;       // two floats, or null: from the parts
+  float* norm;
+  int32_t parts;
+  float max_norm, scale;
+};
+
+struct FoldArgs {
+  RankPtrs in, out;
+  int64_t n;
+  int32_t p, n_out, mean;
+};
+
+// Workgroups of a pass over a batch of tensors, of the first pass over the ranks' buffers.
+// Constants, so that the order of the sums does not depend on the GPU.
+constexpr int kSquaresGrid = 2048;
+constexpr int kFoldGrid = 32768;
+
+int64_t grad_norm_bytes(int64_t n);        // of workspace, for n tensors
+int64_t fold_clip_parts(int64_t n);
+int64_t fold_clip_bytes(int64_t n);        // ... for n elements
+hipError_t launch_grad_norm(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s);
+hipError_t launch_grad_clip(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s);
+hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, int access, void* work, hipStream_t s);
 
 // ---------------------------------------------------------------- errors
 // Sets the calling thread's error message and returns `code` (ra_api.cpp).

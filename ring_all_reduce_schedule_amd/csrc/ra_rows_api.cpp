@@ -1,13 +1,16 @@
 // ra_rows_api.cpp -- C entry points of the row operators declared in include/ra.h
-// (norm, cross entropy, embedding): argument checks, then one call to the
-// launchers in ra_norm.hip, ra_xent.hip and ra_embed.hip.  Nothing here waits,
-// allocates or throws.
+// (norm, cross entropy, log probabilities, embedding) and of the gradients' norm and
+// clipping: argument checks, then one call to the launchers in ra_norm.hip,
+// ra_xent.hip, ra_logprob.hip, ra_embed.hip and ra_grads.hip.  Nothing here waits,
+// allocates device memory or throws.
 #include "ra.h"
 
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "ra_internal.h"
 
@@ -59,6 +62,31 @@ int check_count(const char* what, int n, int lo, int hi) {
   return fail(RA_ERR_INVALID_ARG, "%s = %d, need %d..%d", what, n, lo, hi);
 }
 
+// The bytes [lo, hi) of an array.
+struct Span {
+  uint64_t lo, hi;
+  const char* what;
+  int index;
+  bool write;
+};
+
+// Whether no byte is written by one array and in another.  Sorts the list, unless it is.
+int check_spans(Span* list, int64_t n) {
+  auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(list, list + n, before)) std::sort(list, list + n, before);
+  const Span *read = nullptr, *written = nullptr;   // the ones so far that end last
+  for (int64_t i = 0; i < n; ++i) {
+    const Span& x = list[i];
+    const Span* with = written && x.lo < written->hi         ? written
+                       : x.write && read && x.lo < read->hi ? read
+                                                             : nullptr;
+    if (with) return fail(RA_ERR_ALIAS, "%s (%d) and %s (%d) overlap", with->what, with->index, x.what, x.index);
+    const Span*& last = x.write ? written : read;
+    if (!last || x.hi > last->hi) last = &x;
+  }
+  return RA_OK;
+}
+
 // The arrays of one call: each is present, starts on a boundary of its elements,
 // and shares no byte with another one where either is written.  al() says whether
 // all of them also start on the boundary that the aligned kernels take.
@@ -94,33 +122,13 @@ class Arrays {
     }
     return add(what, index, ptr, bytes, elem, true);
   }
-  int overlaps() {
-    std::sort(list_, list_ + n_, [](const One& a, const One& b) { return a.lo < b.lo; });
-    const One *read = nullptr, *written = nullptr;   // the ones so far that end last
-    for (int i = 0; i < n_; ++i) {
-      const One& x = list_[i];
-      const One* with = written && x.lo < written->hi         ? written
-                        : x.write && read && x.lo < read->hi ? read
-                                                              : nullptr;
-      if (with)
-        return fail(RA_ERR_ALIAS, "%s (%d) and %s (%d) overlap", with->what, with->index, x.what, x.index);
-      const One*& last = x.write ? written : read;
-      if (!last || x.hi > last->hi) last = &x;
-    }
-    return RA_OK;
-  }
+  int overlaps() { return check_spans(list_, n_); }
   bool al() const { return aligned_; }
 
  private:
-  struct One {
-    uint64_t lo, hi;
-    const char* what;
-    int index;
-    bool write;
-  };
   // Three lists of the ranks' (a norm's buffers, outputs and scales) and single arrays.
   static constexpr int kMost = 3 * RA_MAX_RANKS + 16;
-  One list_[kMost];
+  Span list_[kMost];
   int n_ = 0;
   bool aligned_ = true;
 };
@@ -170,11 +178,12 @@ int check_embed_bwd(int64_t tokens, int64_t vocab, int64_t hidden) {
               (long long)hidden);
 }
 
-// Logits and gradients of a cross entropy, and what both directions need of them.
-int check_xent(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype, int target_dtype) {
+// Logits whose vocabulary is cut over the ranks.
+int check_vocab(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
+                const char* index, int index_dtype) {
   int rc = check_ranks(p);
   if (rc == RA_OK) rc = check_real("dtype", dtype);
-  if (rc == RA_OK) rc = check_index("target_dtype", target_dtype);
+  if (rc == RA_OK) rc = check_index(index, index_dtype);
   if (rc == RA_OK) rc = check_rows(tokens, vocab, ra::kXentMaxVocab, "vocab");
   if (rc == RA_OK && (valid < 1 || valid > vocab))
     rc = fail(RA_ERR_INVALID_ARG, "valid = %lld, need 1..vocab = %lld", (long long)valid, (long long)vocab);
@@ -182,17 +191,20 @@ int check_xent(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_
   return rc;
 }
 
-int add_xent(Arrays* to, ra::XentArgs* a, void* const* logits, void* const* grads, int64_t vocab, int64_t valid,
-             int dtype, const void* targets, int target_dtype, const float* dloss, float grad_scale) {
-  const int e = ra::elem_bytes(dtype), p = a->p;
+int check_xent(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype, int target_dtype) {
+  return check_vocab(logits, p, tokens, vocab, valid, dtype, "target_dtype", target_dtype);
+}
+
+// The logits and their gradients (or null), and the geometry of their rows.
+int add_vocab(Arrays* to, ra::VocabArgs* a, void* const* logits, void* const* grads, int p, int64_t tokens,
+              int64_t vocab, int64_t valid, int dtype) {
+  const int e = ra::elem_bytes(dtype);
+  a->p = p;
+  a->tokens = tokens;
   a->cut = {(int32_t)(vocab / p), (int32_t)(vocab % p)};
   a->vocab = (int32_t)vocab;
   a->valid = (int32_t)valid;
-  a->target = targets;
-  a->target64 = target_dtype == RA_INT64;
-  a->dloss = dloss;
-  a->grad_scale = grad_scale;
-  ra::xent_geometry(a);
+  ra::vocab_geometry(a);
   int rc = RA_OK;
   for (int r = 0; r < p && rc == RA_OK; ++r) {
     const int64_t bytes = a->tokens * (a->cut.base + (r < a->cut.extra)) * e;
@@ -206,10 +218,101 @@ int add_xent(Arrays* to, ra::XentArgs* a, void* const* logits, void* const* grad
     else rc = to->add("grads", r, grads[r], bytes, e, true);
     a->dx.b[r] = grads[r];
   }
+  return rc;
+}
+
+int add_xent(Arrays* to, ra::XentArgs* a, void* const* logits, void* const* grads, int p, int64_t tokens,
+             int64_t vocab, int64_t valid, int dtype, const void* targets, int target_dtype, const float* dloss,
+             float grad_scale) {
+  a->target = targets;
+  a->target64 = target_dtype == RA_INT64;
+  a->dloss = dloss;
+  a->grad_scale = grad_scale;
+  int rc = add_vocab(to, a, logits, grads, p, tokens, vocab, valid, dtype);
   const int te = ra::elem_bytes(target_dtype);
   if (rc == RA_OK) rc = to->add("targets", -1, targets, a->tokens * te, te, false, false, 1);
   if (rc == RA_OK) rc = to->add("dloss", -1, dloss, a->tokens * 4, 4, false, true, 1);
   return rc;
+}
+
+int check_positive(const char* what, float x) {
+  if (x > 0.0f && std::isfinite(x)) return RA_OK;
+  return fail(RA_ERR_INVALID_ARG, "%s must be finite and > 0", what);
+}
+
+int check_top(int64_t valid, int top) {
+  if (top < 0) return fail(RA_ERR_INVALID_ARG, "top = %d, need top >= 0", top);
+  if (top > ra::kTopMost) return fail(RA_ERR_UNSUPPORTED, "top = %d exceeds %d", top, ra::kTopMost);
+  if (top > valid) return fail(RA_ERR_INVALID_ARG, "top = %d of %lld valid columns", top, (long long)valid);
+  return RA_OK;
+}
+
+int64_t logprob_bytes(int64_t tokens, int64_t vocab, int p, int top) {
+  return ra::logp_bytes(tokens, ra::logp_splits(tokens, (int)vocab, p), top);
+}
+
+// A norm has to be positive; infinity is one that nothing reaches.
+int check_clip(float max_norm, float scale) {
+  if (!(max_norm > 0.0f)) return fail(RA_ERR_INVALID_ARG, "max_norm must be > 0");
+  return check_positive("scale", scale);
+}
+
+// Tensors of one call, and elements of them all: workgroups and their parts are counted in 32 bits.
+constexpr int64_t kListMost = 1 << 20, kListElements = 1ll << 44;
+
+int check_elements(int64_t n) {
+  if (n < 0) return fail(RA_ERR_INVALID_ARG, "n = %lld, need n >= 0", (long long)n);
+  if (n > kListElements) return fail(RA_ERR_UNSUPPORTED, "n = %lld, at most 2^44 elements", (long long)n);
+  return RA_OK;
+}
+
+int check_list_length(int64_t n) {
+  if (n < 0) return fail(RA_ERR_INVALID_ARG, "n = %lld, need n >= 0", (long long)n);
+  if (n > kListMost)
+    return fail(RA_ERR_UNSUPPORTED, "n = %lld tensors, at most %lld in a call", (long long)n, (long long)kListMost);
+  return RA_OK;
+}
+
+// A list of tensors of any sizes, read, and (outs) what is written for each: the tensor itself or
+// another array.  Neither may share memory with another one that is written.
+int check_list(const ra::TensorListArgs& a, float* norm, void* workspace, int64_t have) {
+  int rc = RA_OK;
+  if (a.n > 0 && (!a.in || !a.counts || !a.types)) return fail(RA_ERR_INVALID_ARG, "tensors, counts or dtypes is NULL");
+  const int64_t need = ra::grad_norm_bytes(a.n);
+  if (have < need)
+    return fail(RA_ERR_INVALID_ARG, "workspace of %lld bytes, need %lld", (long long)have, (long long)need);
+  // host memory, for the call alone
+  std::unique_ptr<Span[]> list(new (std::nothrow) Span[2 * a.n + 2]);
+  if (!list) return fail(RA_ERR_UNSUPPORTED, "no host memory for %lld tensors", (long long)a.n);
+  int64_t m = 0, elements = 0;
+  auto add = [&](const char* what, int64_t i, const void* ptr, int64_t bytes, int elem, bool write) {
+    if (!ptr) return fail(RA_ERR_INVALID_ARG, "%s[%lld] is NULL", what, (long long)i);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(ptr);
+    if (at % elem != 0)
+      return fail(RA_ERR_MISALIGNED, "%s[%lld] = %p is not on a boundary of its %d-byte elements", what, (long long)i,
+                  ptr, elem);
+    list[m++] = {at, at + (uint64_t)bytes, what, (int)i, write};
+    return (int)RA_OK;
+  };
+  for (int64_t i = 0; i < a.n; ++i) {
+    const int64_t count = a.counts[i];
+    if (count < 0) return fail(RA_ERR_INVALID_ARG, "counts[%lld] = %lld", (long long)i, (long long)count);
+    if (count > kListElements || (elements += count) > kListElements)
+      return fail(RA_ERR_UNSUPPORTED, "more than 2^44 elements in a call");
+    rc = check_real("dtype", a.types[i]);
+    if (rc == RA_OK && a.out && a.out_types) rc = check_second("out_dtype", a.out_types[i], a.types[i]);
+    if (rc != RA_OK) return rc;
+    if (count == 0) continue;
+    const int e = ra::elem_bytes(a.types[i]);
+    const int to = a.out && a.out_types ? a.out_types[i] : a.types[i], eo = ra::elem_bytes(to);
+    const bool same = a.out && a.out[i] == a.in[i] && to == a.types[i];
+    rc = add("tensors", i, a.in[i], count * e, e, same);
+    if (rc == RA_OK && a.out && !same) rc = add("outs", i, a.out[i], count * eo, eo, true);
+    if (rc != RA_OK) return rc;
+  }
+  rc = add("norm", 0, norm, 4, 4, true);
+  if (rc == RA_OK) rc = add("workspace", 0, workspace, need, 16, true);
+  return rc == RA_OK ? check_spans(list.get(), m) : rc;
 }
 
 }  // namespace
@@ -368,9 +471,7 @@ int ra_cross_entropy(void* const* logits, int p, int64_t tokens, int64_t vocab, 
   Arrays all;
   ra::XentArgs a;
   std::memset(&a, 0, sizeof a);
-  a.p = p;
-  a.tokens = tokens;
-  rc = add_xent(&all, &a, logits, grads, vocab, valid, dtype, targets, target_dtype, dloss, grad_scale);
+  rc = add_xent(&all, &a, logits, grads, p, tokens, vocab, valid, dtype, targets, target_dtype, dloss, grad_scale);
   if (rc == RA_OK) rc = all.add("loss", -1, loss, tokens * 4, 4, true, true, 1);
   if (rc == RA_OK) rc = all.add("lse", -1, lse, tokens * 4, 4, true, true, 1);
   if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, xent_bytes(tokens, vocab, p, grads != nullptr));
@@ -395,9 +496,7 @@ int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_
   Arrays all;
   ra::XentArgs a;
   std::memset(&a, 0, sizeof a);
-  a.p = p;
-  a.tokens = tokens;
-  rc = add_xent(&all, &a, logits, grads, vocab, valid, dtype, targets, target_dtype, dloss, grad_scale);
+  rc = add_xent(&all, &a, logits, grads, p, tokens, vocab, valid, dtype, targets, target_dtype, dloss, grad_scale);
   if (rc == RA_OK) rc = all.add("lse", -1, lse, tokens * 4, 4, false, false, 1);
   if (rc == RA_OK) rc = all.overlaps();
   if (rc != RA_OK) return rc;
@@ -498,6 +597,177 @@ int ra_embedding_backward(const void* dy, int64_t tokens, int64_t hidden, int dt
   const bool al = all.al() && hidden % 8 == 0;
   debug_rows("embedding_backward", p, tokens, hidden, dtype, al, 1);
   return launched(ra::launch_embed_bwd(a, dtype, dtable_dtype, al, stream));
+}
+
+int ra_token_logprobs_workspace(int64_t tokens, int64_t vocab, int p, int top, int64_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = check_ranks(p);
+  if (rc == RA_OK) rc = check_rows(tokens, vocab, ra::kXentMaxVocab, "vocab");
+  if (rc == RA_OK) rc = check_top(vocab, top);
+  if (rc == RA_OK) *bytes = logprob_bytes(tokens, vocab, p, top);
+  return rc;
+}
+
+int ra_token_logprobs(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
+                      float scale, const void* ids, int id_dtype, float* logprob, float* entropy, float* lse, int top,
+                      void* top_ids, float* top_logprobs, void* workspace, int64_t workspace_bytes,
+                      hipStream_t stream) {
+  int rc = check_vocab(logits, p, tokens, vocab, valid, dtype, "id_dtype", id_dtype);
+  if (rc == RA_OK) rc = check_positive("scale", scale);
+  if (rc == RA_OK) rc = check_top(valid, top);
+  if (rc != RA_OK) return rc;
+  if (tokens == 0) return RA_OK;   // before the next lines: an empty array's address may be NULL
+  if (top > 0 && !top_ids && !top_logprobs) return fail(RA_ERR_INVALID_ARG, "top_ids and top_logprobs are both NULL");
+  if (!logprob && !entropy && !lse && top == 0)
+    return fail(RA_ERR_INVALID_ARG, "logprob, entropy and lse are all NULL, and top is 0");
+  if (logprob && !ids) return fail(RA_ERR_INVALID_ARG, "logprob needs ids");
+  Arrays all;
+  ra::LogpArgs a;
+  std::memset(&a, 0, sizeof a);
+  rc = add_vocab(&all, &a, logits, nullptr, p, tokens, vocab, valid, dtype);
+  const int ei = ra::elem_bytes(id_dtype);
+  if (rc == RA_OK) rc = all.add("ids", -1, ids, tokens * ei, ei, false, true, 1);
+  if (rc == RA_OK) rc = all.add("logprob", -1, logprob, tokens * 4, 4, true, true, 1);
+  if (rc == RA_OK) rc = all.add("entropy", -1, entropy, tokens * 4, 4, true, true, 1);
+  if (rc == RA_OK) rc = all.add("lse", -1, lse, tokens * 4, 4, true, true, 1);
+  if (rc == RA_OK && top > 0) rc = all.add("top_ids", -1, top_ids, tokens * top * ei, ei, true, true, 1);
+  if (rc == RA_OK && top > 0) rc = all.add("top_logprobs", -1, top_logprobs, tokens * top * 4, 4, true, true, 1);
+  if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, logprob_bytes(tokens, vocab, p, top));
+  if (rc == RA_OK) rc = all.overlaps();
+  if (rc != RA_OK) return rc;
+  a.ids = ids;
+  a.ids64 = id_dtype == RA_INT64;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top = top;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.part = static_cast<float*>(workspace);
+  a.scale = scale;
+  a.splits = ra::logp_splits(tokens, (int)vocab, p);
+  const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
+  debug_rows("token_logprobs", p, tokens, vocab, dtype, al, a.splits);
+  return launched(ra::launch_logp(a, dtype, al, stream));
+}
+
+int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
+                               float scale, const void* ids, int id_dtype, const float* lse, const float* entropy,
+                               const float* dlogprob, const float* dentropy, void* const* grads,
+                               hipStream_t stream) {
+  int rc = check_vocab(logits, p, tokens, vocab, valid, dtype, "id_dtype", id_dtype);
+  if (rc == RA_OK) rc = check_positive("scale", scale);
+  if (rc == RA_OK && !grads) rc = fail(RA_ERR_INVALID_ARG, "grads is NULL");
+  if (rc != RA_OK) return rc;
+  if (tokens == 0) return RA_OK;
+  if (!dlogprob && !dentropy) return fail(RA_ERR_INVALID_ARG, "dlogprob and dentropy are both NULL");
+  if (dlogprob && !ids) return fail(RA_ERR_INVALID_ARG, "dlogprob needs ids");
+  if (dentropy && !entropy) return fail(RA_ERR_INVALID_ARG, "dentropy needs entropy");
+  Arrays all;
+  ra::LogpArgs a;
+  std::memset(&a, 0, sizeof a);
+  rc = add_vocab(&all, &a, logits, grads, p, tokens, vocab, valid, dtype);
+  const int ei = ra::elem_bytes(id_dtype);
+  if (rc == RA_OK) rc = all.add("ids", -1, ids, tokens * ei, ei, false, true, 1);
+  if (rc == RA_OK) rc = all.add("lse", -1, lse, tokens * 4, 4, false, false, 1);
+  if (rc == RA_OK) rc = all.add("entropy", -1, entropy, tokens * 4, 4, false, true, 1);
+  if (rc == RA_OK) rc = all.add("dlogprob", -1, dlogprob, tokens * 4, 4, false, true, 1);
+  if (rc == RA_OK) rc = all.add("dentropy", -1, dentropy, tokens * 4, 4, false, true, 1);
+  if (rc == RA_OK) rc = all.overlaps();
+  if (rc != RA_OK) return rc;
+  a.ids = ids;
+  a.ids64 = id_dtype == RA_INT64;
+  a.lse_in = lse;
+  a.entropy_in = entropy;
+  a.dlogprob = dlogprob;
+  a.dentropy = dentropy;
+  a.scale = scale;
+  // A row is cut so that a wave has about four chunks.
+  a.splits = (int32_t)std::max<int64_t>(1, (int64_t)a.total / 16);
+  const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
+  debug_rows("token_logprobs_backward", p, tokens, vocab, dtype, al, a.splits);
+  return launched(ra::launch_logp_bwd(a, dtype, al, stream));
+}
+
+int ra_grad_norm_workspace(int64_t n, int64_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = check_list_length(n);
+  if (rc == RA_OK) *bytes = ra::grad_norm_bytes(n);
+  return rc;
+}
+
+int ra_grad_norm(const void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n, float scale,
+                 float* norm, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  int rc = check_list_length(n);
+  if (rc == RA_OK) rc = check_positive("scale", scale);
+  ra::TensorListArgs a = {tensors, nullptr, counts, dtypes, nullptr, n, n};
+  if (rc == RA_OK) rc = check_list(a, norm, workspace, workspace_bytes);
+  if (rc != RA_OK) return rc;
+  debug_rows("grad_norm", 1, n, 0, n > 0 ? dtypes[0] : 0, false, 1);
+  return launched(ra::launch_grad_norm(a, {nullptr, nullptr, norm, 0, INFINITY, scale}, workspace, stream));
+}
+
+int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n, int64_t counted,
+                 float max_norm, float scale, void* const* outs, const int* out_dtypes, float* norm, void* workspace,
+                 int64_t workspace_bytes, hipStream_t stream) {
+  int rc = check_list_length(n);
+  if (rc == RA_OK && (counted < 0 || counted > n))
+    rc = fail(RA_ERR_INVALID_ARG, "counted = %lld, need 0..n = %lld", (long long)counted, (long long)n);
+  if (rc == RA_OK) rc = check_clip(max_norm, scale);
+  ra::TensorListArgs a = {tensors, outs ? outs : tensors, counts, dtypes, outs ? out_dtypes : nullptr, n, counted};
+  if (rc == RA_OK) rc = check_list(a, norm, workspace, workspace_bytes);
+  if (rc != RA_OK) return rc;
+  debug_rows("grad_clip", 1, n, 0, n > 0 ? dtypes[0] : 0, false, 1);
+  return launched(ra::launch_grad_clip(a, {nullptr, nullptr, norm, 0, max_norm, scale}, workspace, stream));
+}
+
+int ra_allreduce_clip_workspace(int64_t n, int64_t* bytes) {
+  if (!bytes) return fail(RA_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = check_elements(n);
+  if (rc == RA_OK) *bytes = ra::fold_clip_bytes(n);
+  return rc;
+}
+
+int ra_allreduce_clip(void* const* bufs, int p, int64_t n, int dtype, int op, float max_norm, float scale,
+                      void* const* outs, int n_out, float* norm, void* workspace, int64_t workspace_bytes,
+                      hipStream_t stream) {
+  int rc = check_ranks(p);
+  if (rc == RA_OK) rc = check_real("dtype", dtype);
+  if (rc == RA_OK) rc = check_elements(n);
+  if (rc == RA_OK) rc = check_count("n_out", n_out, 1, p);
+  if (rc == RA_OK) rc = check_clip(max_norm, scale);
+  if (rc != RA_OK) return rc;
+  if (op != RA_SUM && op != RA_AVG) {
+    if (op != RA_MAX) return fail(RA_ERR_INVALID_ARG, "unknown op %d", op);
+    return fail(RA_ERR_UNSUPPORTED, "op %d: need RA_SUM or RA_AVG", op);
+  }
+  const int e = ra::elem_bytes(dtype);
+  Arrays all;
+  ra::FoldArgs a;
+  std::memset(&a, 0, sizeof a);
+  if (n > 0) {
+    rc = add_ranks(&all, "bufs", bufs, p, n * e, e, false, &a.in);
+    if (rc == RA_OK && !outs) rc = fail(RA_ERR_INVALID_ARG, "outs is NULL");
+    for (int r = 0; r < n_out && rc == RA_OK; ++r) {
+      // a rank's output may take the place of a rank's buffer
+      bool same = false;
+      for (int q = 0; q < p; ++q) same = same || outs[r] == bufs[q];
+      rc = same ? all.add_or_same("outs", r, outs[r], n * e, e) : all.add("outs", r, outs[r], n * e, e, true);
+      a.out.b[r] = outs[r];
+    }
+  }
+  const bool al = all.al() && n % 8 == 0;
+  if (rc == RA_OK) rc = all.add("norm", -1, norm, 4, 4, true);
+  if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, ra::fold_clip_bytes(n));
+  if (rc == RA_OK) rc = all.overlaps();
+  if (rc != RA_OK) return rc;
+  a.n = n;
+  a.p = p;
+  a.n_out = n_out;
+  a.mean = op == RA_AVG;
+  debug_rows("allreduce_clip", p, n, 1, dtype, al, 1);
+  return launched(ra::launch_fold_clip(a, dtype, {nullptr, nullptr, norm, 0, max_norm, scale},
+                                       access_of(al, n * e * (p + n_out)), workspace, stream));
 }
 
 }  // extern "C"

@@ -35,17 +35,10 @@
 // left; which part of the memory system is, no counter has shown.  The float32 kernels
 // with eight units a lane fill the registers (two of 128 go to scratch), and with long
 // rows stay at 4.5-4.7 TB/s.
-#include "ra_rows.h"
+#include "ra_vocab.h"
 
 namespace ra {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
-__device__ __forceinline__ float log2_of(float x) { return __builtin_amdgcn_logf(x); }
 
 // A sum z of exponentials relative to 2^c.  An empty one is (kNone, 0).
 struct Part {
@@ -68,124 +61,6 @@ __device__ __forceinline__ Part block_join(Part a, Part* lds, int waves) {
   Part b = lane % 16 < waves ? lds[lane % 16] : Part{kNone, 0.0f};
   const float c = row_max(b.c);
   return {lane_value(c, 0), lane_value(row_sum(b.z * exp2_of(b.c - c)), 0)};
-}
-
-// A row's units over all ranks go in chunks of 64, one to each lane of a wave; a
-// chunk lies in one piece, so that its pointers are the wave's and not the lanes'.
-// First come the chunks of whole 512 columns, a.whole of each piece, in the order
-// of their columns; then what is left of each piece, if anything is.
-struct Chunk {
-  int r;        // piece (rank)
-  int len;      // the piece's columns
-  int c0;       // the chunk's first column in its piece
-  int col0;     // ... and in the vocabulary
-};
-constexpr int kChunk = 64 * kU;
-
-__device__ __forceinline__ Chunk chunk(const XentArgs& a, int q) {
-  // Computed where it is used: kept over a row's passes, the places of sixteen
-  // chunks would not fit the scalar registers.
-  asm volatile("" : "+s"(q));
-  Chunk s;
-  const int wholes = a.whole * a.p;
-  if (q < wholes) {
-    s.r = a.whole == 1 ? q : (int)__umulhi((uint32_t)q, a.magic);
-    s.c0 = (q - s.r * a.whole) * kChunk;
-  } else {
-    s.r = q - wholes;
-    s.c0 = a.whole * kChunk;
-  }
-  s.len = piece_len(a.cut, s.r);
-  s.col0 = piece_lo(a.cut, s.r) + s.c0;
-  return s;
-}
-
-// How a kernel reads and writes units.
-enum Mode {
-  kAligned,   // rows of whole units on 16-byte boundaries
-  kOdd,       // any rows of pieces of at least a unit
-  kTiny       // pieces shorter than a unit are among them: element by element
-};
-
-// The lane's unit of a chunk: it loads elements [c, c + 8) of the piece's row,
-// and its own are those from `from` on that the piece has.  The unit that would
-// pass the row's end is moved back to end there, and so are the units of lanes
-// behind it, which then own nothing: every lane loads without a branch.
-struct Lane {
-  int c, from;
-};
-template <int MODE>
-__device__ __forceinline__ Lane lane_of(const Chunk& s) {
-  const int from = s.c0 + (int)(threadIdx.x % 64) * kU;
-  if (MODE == kTiny) return {from, from};
-  return {min(from, s.len - kU), from};
-}
-
-// Which elements count: the lane's own, before the first column that is not valid.
-__device__ __forceinline__ bool counts(const Chunk& s, const Lane& l, int valid, int i) {
-  return l.c + i >= l.from && l.c + i < s.len && s.col0 - s.c0 + l.c + i < valid;
-}
-
-// Element i of a unit becomes -inf.
-template <int DT>
-__device__ __forceinline__ void mask_out(Unit<DT>* t, int i) {
-  if constexpr (DT == 1) {
-    t->v[i / 4][i % 4] = 0xff800000u;
-  } else {
-    const uint32_t ninf = DT == 2 ? 0xff80u : 0xfc00u;
-    const uint32_t w = t->v[0][i / 2];
-    t->v[0][i / 2] = i % 2 ? (w & 0xffffu) | ninf << 16 : (w & 0xffff0000u) | ninf;
-  }
-}
-
-// The lane's unit of a chunk as memory holds it.
-template <int DT, int MODE>
-__device__ __forceinline__ Unit<DT> fetch(const XentArgs& a, int64_t row, const Chunk& s) {
-  const char* x = static_cast<const char*>(a.x.b[s.r]) + row * s.len * ElemSize<DT>::value;
-  const Lane l = lane_of<MODE>(s);
-  if constexpr (MODE != kTiny) {
-    return load_unit<DT, MODE == kAligned>(x, l.c);
-  } else {
-    return load_cut<DT, false>(x, 0, {l.c, 0, max(0, min(kU, s.len - l.c))});
-  }
-}
-
-// ... with -inf for what does not count: the first a.full chunks count as a whole.
-template <int DT, int MODE>
-__device__ __forceinline__ void mask(Unit<DT>* t, const XentArgs& a, int q, const Chunk& s) {
-  if (q < a.full) return;
-  const Lane l = lane_of<MODE>(s);
-#pragma unroll
-  for (int i = 0; i < kU; ++i)
-    if (!counts(s, l, a.valid, i)) mask_out<DT>(t, i);
-}
-
-template <int DT>
-__device__ __forceinline__ void mask_all(Unit<DT>* t) {
-#pragma unroll
-  for (int i = 0; i < kU; ++i) mask_out<DT>(t, i);
-}
-
-// The masked units of N chunks q0, q0 + step, ...; -inf from chunk `end` on.  All
-// loads go out before the first is looked at.
-template <int DT, int MODE, int N>
-__device__ __forceinline__ void fetch_all(Unit<DT>* u, const XentArgs& a, int64_t row, int q0, int step, int end) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) u[k] = fetch<DT, MODE>(a, row, chunk(a, min(q0 + k * step, end - 1)));
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int q = q0 + k * step;
-    if (q < end) mask<DT, MODE>(&u[k], a, q, chunk(a, q));
-    else mask_all<DT>(&u[k]);
-  }
-}
-
-// Keeps the compiler from holding on to a unit's unpacked values: they would take
-// twice the unit's registers from one pass over it to the next.
-template <int DT>
-__device__ __forceinline__ void forget(Unit<DT>* t) {
-  asm volatile("" : "+v"(t->v[0]));
-  if constexpr (DT == 1) asm volatile("" : "+v"(t->v[1]));
 }
 
 // About the largest of N units' values, from kNone up.
@@ -231,8 +106,6 @@ __device__ __forceinline__ void take(Part& t, Unit<DT>* u) {
   }
 }
 
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
-
 // One token: its target, and what its gradient is scaled with.
 constexpr int kNoLoss = -1, kNoColumn = -2;
 struct Token {
@@ -247,17 +120,6 @@ __device__ __forceinline__ Token token(const XentArgs& a, int64_t row) {
   t.k = a.grad_scale * (a.dloss ? a.dloss[row] : 1.0f);
   if (t.y == kNoColumn) t.k = __uint_as_float(0x7fc00000u);
   return t;
-}
-
-// The target's logit; not read where there is none.
-template <int DT>
-__device__ __forceinline__ float logit(const XentArgs& a, int64_t row, int y) {
-  if (y < 0) return 0.0f;
-  const int r = piece_of(a.cut, y);
-  const typename Elem<DT>::S* x = static_cast<const typename Elem<DT>::S*>(a.x.b[r]);
-  const int64_t at = row * piece_len(a.cut, r) + (y - piece_lo(a.cut, r));
-  if constexpr (DT == 1) return __uint_as_float(x[at]);
-  else return Elem<DT>::to_w(x[at]);
 }
 
 // A row's sum: relative to 2^c, or (plain) to e^c with c the largest logit.
@@ -318,17 +180,6 @@ struct Grad {
 };
 __device__ __forceinline__ Grad grad_of(const Token& t, const Sum& sum) {
   return {empty(sum) ? 0.0f : sum.c, t.k / sum.z, sum.plain, t.y == kNoLoss || (t.y >= 0 && empty(sum))};
-}
-
-// Writes a lane's own elements of a chunk's gradient.  WHOLE: 512 columns.
-template <int DT, int MODE, bool WHOLE>
-__device__ __forceinline__ void put(const XentArgs& a, int64_t row, const Chunk& s, const Lane& l, const Unit<DT>& t) {
-  char* dx = static_cast<char*>(a.dx.b[s.r]) + row * s.len * ElemSize<DT>::value;
-  if (WHOLE) {
-    store_unit<DT, MODE == kAligned>(dx, l.from, t);
-  } else if (l.from < s.len) {
-    store_cut<DT, MODE == kAligned>(dx, 0, {l.c, l.from - l.c, min(kU, s.len - l.c)}, t);
-  }
 }
 
 // The gradient of a wave's chunk.  WHOLE: one of the first a.full.  One chunk of
@@ -674,11 +525,11 @@ hipError_t bwd_go(const XentArgs& a, bool al, hipStream_t s) {
 }  // namespace
 
 // The chunks of a cut vocabulary.
-static int total_chunks(int vocab, int p) { return vocab / p / kChunk * p + (vocab % (p * kChunk) != 0 ? p : 0); }
+int vocab_chunks(int vocab, int p) { return vocab / p / kChunk * p + (vocab % (p * kChunk) != 0 ? p : 0); }
 
-void xent_geometry(XentArgs* a) {
+void vocab_geometry(VocabArgs* a) {
   a->whole = a->cut.base / kChunk;
-  a->total = total_chunks(a->vocab, a->p);
+  a->total = vocab_chunks(a->vocab, a->p);
   a->magic = a->whole > 0 ? (uint32_t)(((1ull << 32) + a->whole - 1) / a->whole) : 0;
   // chunks come in the order of their columns: the first ones end before `valid`
   a->full = 0;
@@ -699,7 +550,7 @@ int64_t xent_words(int64_t tokens, int splits) { return splits > 1 ? tokens * (k
 //   gradient  128000: 1 token 9.4 / 20.6, 128 25.4 / 24.8;  32000: 64 11.8 / 13.6, 128 16.6 / 14.6
 //               8192: 1 token 8.1 / 9.3, 192 9.9 / 10.0
 int xent_splits(int64_t tokens, int vocab, int p, bool grad) {
-  const int chunks = total_chunks(vocab, p);
+  const int chunks = vocab_chunks(vocab, p);
   if (tokens < 1) return 1;      // the workspace of an empty batch is asked for, too
   if (vocab / p < kU || (grad ? tokens > 96 : chunks <= 64 || tokens > chunks / 2)) return 1;
   // two chunks at least for each wave of a row's workgroups

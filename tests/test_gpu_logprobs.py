@@ -1,0 +1,256 @@
+"""ra_token_logprobs and its backward against their 64-bit forms (tests/answers_ref.py)."""
+
+import math
+
+import pytest
+import torch
+
+from ring_all_reduce_schedule_amd import binding as B
+from tests import answers_ref as A
+from tests import rows_ref as R
+from tests.gpu_util import require_gpu
+from tests.pads import cut, padded, untouched
+
+pytestmark = pytest.mark.gpu
+
+T = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def make(t, v, dtype, seed, valid, itype=torch.int64):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (3 * torch.randn((t, v), device="cuda", generator=g)).to(dtype)
+    y = torch.randint(0, valid, (t,), device="cuda", generator=g).to(itype)
+    y[torch.rand(t, device="cuda", generator=g) < 0.2] = -1
+    return x, y, g
+
+
+def special_rows(x, y, valid, dtype):
+    """Rows that a mask, a model gone wrong or ties make, as far as there are rows."""
+    t, v = x.shape
+    low = torch.finfo(dtype).min
+
+    def each():
+        x[0, : valid // 2] = -math.inf             # masked columns
+        yield
+        x[1, 1:valid] = low                        # masked with the type's lowest value
+        yield
+        x[2, :valid] = low                         # all of them
+        yield
+        x[3, :valid] = -math.inf                   # nothing left
+        yield
+        x[4, :valid] = 1.5                         # all equal
+        yield
+        x[5, :valid] = -math.inf                   # a grammar leaves three
+        x[5, torch.tensor([0, valid // 2, valid - 1])] = torch.tensor([1.0, 3.0, 2.0], dtype=dtype, device="cuda")
+        yield
+        x[6, valid // 3] = math.nan
+        yield
+        x[7, valid // 3] = math.inf
+        yield
+        x[8, :valid] = torch.where(x[8, :valid] > 0, 0.0, -0.0)    # zeros of both signs
+        yield
+        x[9, :valid] = x[9, :valid].round()        # few values
+        yield
+        x[10] *= 100                               # one column has it all
+        yield
+        y[11] = valid                              # no column
+        yield
+    for _, _ in zip(range(t), each()):
+        pass
+    if valid < v:
+        x[:, valid:] = math.nan                    # padding is not read
+
+
+CASES = [
+    # p, tokens, vocab, valid, top, dtype, offset
+    (1, 1, 1, 1, 1, "f32", 0), (2, 3, 1, 1, 1, "bf16", 0), (4, 12, 3, 2, 2, "f16", 0), (3, 14, 20, 20, 20, "bf16", 0),
+    (64, 13, 100, 100, 64, "bf16", 0), (64, 13, 500, 499, 64, "f32", 0), (1, 12, 64, 64, 64, "f16", 1),
+    (1, 2, 511, 511, 5, "f32", 0), (1, 15, 512, 512, 20, "bf16", 0), (1, 15, 513, 500, 64, "f16", 0),
+    (2, 300, 1024, 1000, 20, "bf16", 0), (8, 213, 4096, 4096, 5, "bf16", 0), (8, 40, 4100, 4099, 64, "bf16", 0),
+    (9, 230, 5003, 5003, 20, "f16", 1), (64, 115, 2000, 1999, 64, "f32", 0), (64, 13, 32000, 32000, 20, "bf16", 0),
+    (8, 1, 128000, 128000, 20, "bf16", 0), (8, 14, 128000, 128000, 64, "f16", 0), (9, 13, 50017, 50001, 64, "f32", 0),
+    (4, 1, 32000, 32000, 5, "f16", 0), (8, 65, 32768, 32768, 20, "bf16", 0), (8, 130, 16384, 16380, 20, "f32", 3),
+    (4, 140, 33000, 33000, 1, "f32", 0), (8, 140, 65536, 65536, 64, "bf16", 0), (3, 113, 70001, 70000, 20, "bf16", 1),
+    (8, 134, 131072, 131072, 20, "bf16", 0), (1, 150, 151_937, 151_900, 64, "f16", 0), (2, 150, 140_000, 140_000, 20, "f32", 0),
+    (8, 300, 295_000, 295_000, 20, "bf16", 0), (5, 330, 300_007, 300_000, 64, "f16", 0), (3, 13, 1_000_003, 1_000_000, 64, "bf16", 0),
+    (63, 3, 1 << 24, 1 << 24, 64, "bf16", 0), (2, 12, 1 << 20, 1 << 20, 20, "f32", 0),
+]
+
+
+@pytest.mark.parametrize("p,t,v,valid,top,dt,off", CASES)
+def test_logprobs(p, t, v, valid, top, dt, off):
+    require_gpu()
+    dtype = T[dt]
+    itype = torch.int32 if t % 2 else torch.int64
+    x, y, _ = make(t, v, dtype, t + v, valid, itype)
+    special_rows(x, y, valid, dtype)
+    scale = [1.0, 0.7, 2.5][t % 3]
+    logits = cut(x, p, off)
+    keep = [c.clone() for c in logits]
+    f = dict(dtype=torch.float32)
+    lp, ent, lse = (padded((t,), torch.float32, 1) for _ in range(3))
+    ids, tlp = padded((t, top), itype, 1), padded((t, top), torch.float32, 1)
+    want, err = A.logprobs(x, y, scale, valid, top)
+    print(f"[case] logprobs p={p} t={t} v={v} top={top} {dt}", flush=True)
+    B.ra_token_logprobs(logits, y, lp, ent, lse, ids, tlp, scale=scale, valid=valid)
+    torch.cuda.synchronize()
+    assert torch.equal(ids.long(), want[3])
+    for got, w, e, what in ((lp, want[0], err[0], "logprob"), (ent, want[1], err[1], "entropy"),
+                            (lse, want[2], err[2], "lse"), (tlp, want[4], err[4], "top_logprobs")):
+        R.check(got, w, R.rounded(torch.where(w.isfinite(), w, 0.0), e, torch.float32), what)
+    for a in (lp, ent, lse, ids, tlp):
+        untouched(a)
+    for a, b in zip(logits, keep):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    # without the alternatives, and each output alone: the same bits
+    one, two, three = (torch.empty(t, device="cuda", **f) for _ in range(3))
+    B.ra_token_logprobs(logits, y, one, two, three, scale=scale, valid=valid)
+    for a, b in ((one, lp), (two, ent), (three, lse)):
+        assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+    ids2 = torch.empty((t, top), dtype=itype, device="cuda")
+    B.ra_token_logprobs(logits, top_ids=ids2, scale=scale, valid=valid)
+    assert torch.equal(ids2, ids)
+    tlp2 = torch.empty((t, top), device="cuda", **f)
+    B.ra_token_logprobs(logits, top_logprobs=tlp2, scale=scale, valid=valid)
+    assert torch.equal(tlp2.nan_to_num(7.0), tlp.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("t,v,dt", [(3, 131072, "bf16"), (300, 131072, "bf16"), (300, 4096, "f32"), (300, 50017, "f16")])
+def test_best_columns_that_few_threads_hold(t, v, dt):
+    """More columns beat the others, in fewer threads, than the first bound is made for: eight of every 512."""
+    require_gpu()
+    dtype = T[dt]
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = torch.randn((t, v), device="cuda", generator=g)
+    col = torch.arange(v, device="cuda")
+    x += torch.where(col % 512 < 8, 100.0, 0.0) + torch.where((col % 512 >= 8) & (col % 512 < 16), 50.0, 0.0)
+    x[::2, ::512] = 200.0                                     # and ties among them
+    x = x.to(dtype)
+    ids = torch.empty((t, 64), dtype=torch.int64, device="cuda")
+    print(f"[case] crowded columns t={t} v={v} {dt}", flush=True)
+    B.ra_token_logprobs(cut(x, 2), top_ids=ids)
+    assert torch.equal(ids, A.best(x, 64))
+    B.ra_token_logprobs(cut(x, 2), top_ids=ids[:, :1].contiguous())
+    few = torch.empty((t, 3), dtype=torch.int64, device="cuda")
+    B.ra_token_logprobs(cut(x, 8), top_ids=few)
+    assert torch.equal(few, A.best(x, 3))
+
+
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e8, 1e12, 1e30])
+@pytest.mark.parametrize("v", [1000, 40000])
+@pytest.mark.parametrize("t", [2, 150])
+def test_logits_of_any_size(size, v, t):
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(v + t)
+    x = torch.randn((t, v), device="cuda", generator=g) * size + size
+    y = torch.randint(0, v, (t,), device="cuda", generator=g)
+    lp, ent, lse = (torch.empty(t, device="cuda") for _ in range(3))
+    ids, tlp = torch.empty((t, 5), dtype=torch.int64, device="cuda"), torch.empty((t, 5), device="cuda")
+    B.ra_token_logprobs(cut(x, 4), y, lp, ent, lse, ids, tlp)
+    want, err = A.logprobs(x, y, 1.0, v, 5)
+    assert torch.equal(ids, want[3])
+    for got, w, e, what in ((lp, want[0], err[0], "logprob"), (ent, want[1], err[1], "entropy"),
+                            (lse, want[2], err[2], "lse"), (tlp, want[4], err[4], "top_logprobs")):
+        R.check(got, w, R.rounded(w, e, torch.float32), what)
+
+
+BACKWARD = [c for c in CASES if c[0:3] not in ((63, 3, 1 << 24),)]
+
+
+@pytest.mark.parametrize("p,t,v,valid,top,dt,off", BACKWARD)
+@pytest.mark.parametrize("which", ["both", "logprob", "entropy", "in place"])
+def test_logprobs_backward(p, t, v, valid, top, dt, off, which):
+    require_gpu()
+    dtype = T[dt]
+    itype = torch.int32 if t % 2 else torch.int64
+    x, y, g = make(t, v, dtype, t + v, valid, itype)
+    special_rows(x, y, valid, dtype)
+    scale = [1.0, 0.7, 2.5][t % 3]
+    want, _ = A.logprobs(x, y, scale, valid, 0)
+    lse, ent = want[2].float(), want[1].float()
+    da = torch.randn(t, device="cuda", generator=g)
+    db = 0.1 * torch.randn(t, device="cuda", generator=g)
+    if t > 12:
+        da[12] = db[12] = 0.0
+        x[12, valid // 2] = math.nan                  # weighs nothing: zeros
+        lse[12] = ent[12] = math.nan
+    if which == "logprob":
+        db = None
+    if which == "entropy":
+        da = None
+    ids = None if which == "entropy" and t % 2 else y
+    logits = cut(x, p, off)
+    b = B.ra_chunk_bounds(v, p)
+    grads = logits if which == "in place" else [padded((t, b[r + 1] - b[r]), dtype, off) for r in range(p)]
+    print(f"[case] logprobs backward p={p} t={t} v={v} {dt} {which}", flush=True)
+    B.ra_token_logprobs_backward(logits, ids, lse, grads, da, None if db is None else ent, db, scale=scale, valid=valid)
+    torch.cuda.synchronize()
+    # where only the entropy's weight counts, an id that no column is is no matter
+    wy = None if da is None else y
+    d, e = A.logprobs_backward(x, wy, lse, ent, da, db, scale, valid)
+    got = torch.cat([c.to(R.F64) for c in grads], 1)
+    R.check(got, d, R.rounded(torch.where(d.isfinite(), d, 0.0), e, dtype), "grads")
+    for c in grads:
+        untouched(c)
+
+
+def test_gradient_is_the_forward_calls_slope():
+    """By differences of the library's own results in many directions, and against autograd in 64 bits."""
+    require_gpu()
+    t, v, scale = 6, 700, 0.8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((t, v), device="cuda", generator=g)
+    y = torch.randint(0, v, (t,), device="cuda", generator=g)
+    da, db = torch.randn(t, device="cuda", generator=g), torch.randn(t, device="cuda", generator=g)
+
+    def forward(x):
+        out = [torch.empty(t, device="cuda") for _ in range(3)]
+        B.ra_token_logprobs(cut(x, 3), y, *out, scale=scale)
+        return out
+    lp, ent, lse = forward(x)
+    grads = [torch.empty_like(c) for c in cut(x, 3)]
+    B.ra_token_logprobs_backward(cut(x, 3), y, lse, grads, da, ent, db, scale=scale)
+    got = torch.cat(grads, 1).double()
+    z = x.double().requires_grad_()
+    ln_p = torch.log_softmax(z * float(torch.tensor(scale)), 1)
+    value = (da * ln_p.gather(1, y.unsqueeze(1)).squeeze(1)).sum() - (db.unsqueeze(1) * ln_p.exp() * ln_p).sum()
+    value.backward()
+    d, e = A.logprobs_backward(x, y, lse, ent, da, db, scale, v)
+    # lse and the entropy as float32 have them: off by 2^-23 of some 7, times a gradient
+    R.check(got, z.grad, e + 2.0 ** -20 * (d.abs() + z.grad.abs()) + 2.0 ** -24, "grads")
+    h = 2.0 ** -4
+    for seed in range(8):
+        step = torch.randn((t, v), device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
+        up, down = forward(x + h * step), forward(x - h * step)
+        slope = sum(((a * (u.double() - w.double()))).sum() for a, u, w in zip((da, db), up, down)) / (2 * h)
+        want = (got * step.double()).sum()
+        # a difference's own error: h^2/6 times a third derivative (of order one, along the step, for each
+        # token), and float32's of some 7 over h
+        assert abs(float(slope - want)) <= t * (h * h + 100 * 2.0 ** -24 / h)
+
+
+def test_an_empty_batch():
+    require_gpu()
+    e = torch.empty
+    for p, v in ((1, 8), (3, 50000), (2, 1 << 24)):
+        b = B.ra_chunk_bounds(v, p)
+        x = [e((0, b[r + 1] - b[r]), device="cuda") for r in range(p)]
+        y, f = e(0, dtype=torch.int64, device="cuda"), e(0, device="cuda")
+        B.ra_token_logprobs(x, y, f, f, f, e((0, 5), dtype=torch.int64, device="cuda"), e((0, 5), device="cuda"))
+        B.ra_token_logprobs_backward(x, y, f, x, dlogprob=f)
+
+
+def test_results_do_not_depend_on_how_the_vocabulary_is_cut():
+    """The best columns are the same for every cut, and so are repeated calls' bits."""
+    require_gpu()
+    t, v = 20, 9000
+    x, y, _ = make(t, v, torch.bfloat16, 9, v)
+    ids = [torch.empty((t, 64), dtype=torch.int64, device="cuda") for _ in range(5)]
+    for p, i in zip((1, 2, 8, 9, 64), ids):
+        B.ra_token_logprobs(cut(x, p), y, top_ids=i)
+        assert torch.equal(i, ids[0])
+    logits = cut(x, 8)
+    outs = [[torch.empty(t, device="cuda") for _ in range(3)] for _ in range(4)]
+    for o in outs:
+        B.ra_token_logprobs(logits, y, *o)
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
