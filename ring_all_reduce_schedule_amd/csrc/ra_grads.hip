@@ -19,8 +19,6 @@ namespace ra {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileUnits = 4;                                  // of a thread
-constexpr int kTile = kThreads * kTileUnits * kU;              // elements
 
 __device__ __forceinline__ double wave_sum64(double x) {
 #pragma unroll
@@ -80,169 +78,385 @@ __global__ __launch_bounds__(1024) void k_finish(ClipRule r, float* to) {
   }
 }
 
-// ---------------------------------------------------------------- many tensors
+// ---------------------------------------------------------------- elements
 
-static_assert(sizeof(TensorBatch) + sizeof(ClipRule) + 16 <= 4096, "a launch's arguments");
-
-// The tensor of a batch that has tile t.
-__device__ __forceinline__ int tensor_of(const TensorBatch& b, uint32_t t) {
-  int n = 0;
-  for (int i = 0; i < kBatchTensors; i += 64)
-    n += __builtin_popcountll(__ballot(b.first[i + threadIdx.x % 64 + 1] <= t));
-  return __builtin_amdgcn_readfirstlane(n);
+// A lane moves N consecutive elements of each array at a time, at most 16 bytes, so that a wave's
+// accesses are whole lines: 8 elements, or 4 where one of the arrays is float32.  (A lane that
+// moved 8 float32, as two accesses 16 bytes apart, wrote half lines: 889 us where it is 497 now,
+// 8 x 256 MiB.)  Arrays start on any boundary of their elements, for which gfx950 issues the same
+// accesses.  Where a run of elements ends inside a lane's, those are moved back to end there, and
+// the first `lo` of them, which are another lane's, are loaded and not used.  Runs shorter than N
+// go a lane to an element.
+template <int N> struct Some {
+  float x[N];
+};
+struct Own {
+  int at, lo;         // elements [at + lo, at + N) are the lane's
+};
+template <int N>
+__device__ __forceinline__ Own own_of(int j, int len) {
+  const int at = min(j * N, len - N);
+  return {at, j * N - at};
 }
 
-// The tiles of a workgroup: [lo, hi).
-__device__ __forceinline__ void tile_range(uint32_t tiles, uint32_t* lo, uint32_t* hi) {
-  *lo = (uint32_t)((uint64_t)tiles * blockIdx.x / gridDim.x);
-  *hi = (uint32_t)((uint64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+typedef uint32_t u32x2_by2 __attribute__((ext_vector_type(2), aligned(2)));
+
+// What a lane's N elements are in registers and in memory.
+template <int DT, int N> struct Word { typedef u32x2 R; typedef u32x2_by2 M; };
+template <> struct Word<1, 4> { typedef u32x4 R; typedef u32x4_by4 M; };
+template <int DT> struct Word<DT, 8> { typedef u32x4 R; typedef u32x4_by2 M; };
+
+// NT: past the caches.
+template <int DT, int N, bool NT>
+__device__ __forceinline__ typename Word<DT, N>::R load_word(const void* p, int64_t i) {
+  typedef typename Word<DT, N>::M M;
+  const M* q = reinterpret_cast<const M*>(static_cast<const char*>(p) + i * ElemSize<DT>::value);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  else return *q;
 }
 
-// The thread's units of a tile of `len` elements at x.
-template <int DT>
-__device__ __forceinline__ void load_tile(Unit<DT>* t, const void* x, int len) {
+template <int DT, int N>
+__device__ __forceinline__ Some<N> values(const typename Word<DT, N>::R w) {
+  Some<N> s;
 #pragma unroll
-  for (int u = 0; u < kTileUnits; ++u) {
-    const int j = threadIdx.x + u * kThreads;
-    t[u] = Unit<DT>{};
-    if (j * kU < len) t[u] = load_cut<DT, kOddRows>(x, 0, unit_cut<kOddRows>(j, len));
+  for (int k = 0; k < N; ++k) {
+    if constexpr (DT == 1) s.x[k] = __uint_as_float(w[k]);
+    else if constexpr (DT == 2) s.x[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+    else s.x[k] = f16_to_f32((uint16_t)(w[k / 2] >> (k % 2 * 16)));
+  }
+  return s;
+}
+
+// Rounded to nearest, ties to even.
+template <int DT, int N>
+__device__ __forceinline__ typename Word<DT, N>::R word_of(const Some<N>& s) {
+  typename Word<DT, N>::R w;
+  if constexpr (DT == 1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = __float_as_uint(s.x[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) {
+      const f32x2 two = {s.x[2 * k], s.x[2 * k + 1]};
+      if constexpr (DT == 2) w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+      else w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, f16x2));
+    }
+  }
+  return w;
+}
+
+// The lane's elements of the run at element `run` of p.
+template <int DT, int N, bool NT>
+__device__ __forceinline__ void store_own(void* p, int64_t run, const Own& o, const typename Word<DT, N>::R w) {
+  typedef typename Elem<DT>::S S;
+  S* q = static_cast<S*>(p) + run + o.at;
+  if (o.lo == 0) {
+    typedef typename Word<DT, N>::M M;
+    if constexpr (NT) __builtin_nontemporal_store((M)w, reinterpret_cast<M*>(q));
+    else *reinterpret_cast<M*>(q) = w;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k < o.lo) continue;
+    if constexpr (DT == 1) q[k] = w[k];
+    else q[k] = (S)(w[k / 2] >> (k % 2 * 16));
   }
 }
 
+// One element.
 template <int DT>
-__device__ __forceinline__ void add_squares(double* acc, const Unit<DT>& t, const Cut& cut) {
+__device__ __forceinline__ float value_of(typename Elem<DT>::S x) {
+  if constexpr (DT == 1) return __uint_as_float(x);
+  else return Elem<DT>::to_w(x);
+}
+template <int DT>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+  return value_of<DT>(static_cast<const typename Elem<DT>::S*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ typename Elem<DT>::S one_of(float x) {
+  if constexpr (DT == 1) return __float_as_uint(x);
+  else return Elem<DT>::from_w(x);
+}
+template <int DT>
+__device__ __forceinline__ void store_one(void* p, int64_t i, float x) {
+  static_cast<typename Elem<DT>::S*>(p)[i] = one_of<DT>(x);
+}
+
+template <int N>
+__device__ __forceinline__ void add_squares(double* acc, const Some<N>& s, int lo) {
 #pragma unroll
-  for (int k = 0; k < kU; ++k) {
-    const double x = owns<kOddRows>(cut, k) ? (double)unit_get<DT>(t, k) : 0.0;
+  for (int k = 0; k < N; ++k) {
+    const double x = k >= lo ? (double)s.x[k] : 0.0;
     acc[k % 4] = __builtin_fma(x, x, acc[k % 4]);
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void tile_squares(double* acc, const void* x, int len) {
-  Unit<DT> t[kTileUnits];
-  load_tile<DT>(t, x, len);
+// ---------------------------------------------------------------- many tensors
+
+constexpr int kTile = kThreads * 32;       // elements that a workgroup takes of a tensor at a time
+
+// The tensors of a launch, whose arguments have to stay under 4 KiB: cut into tiles, which
+// go one tensor's behind the other's.
+template <int N, bool OUT> struct Batch {
+  const void* in[N];
+  void* out[OUT ? N : 1];
+  uint32_t first[N + 1];    // tiles before each tensor's; from the last one on, all tiles
+  uint16_t last[N];         // elements of a tensor's last tile, less 1, and its Kind
+};
+typedef Batch<256, false> Read;
+typedef Batch<176, true> Scale;
+enum Kind { kHalf = 1 << 13, kFull = 1 << 14, kWiden = 1 << 15 };   // float16 (neither: bfloat16), float32; out is float32
+static_assert(kTile <= kHalf, "a last tile's elements have 13 bits");
+static_assert(sizeof(Read) + sizeof(ClipRule) + 16 <= 4096 && sizeof(Scale) + sizeof(ClipRule) + 16 <= 4096, "arguments");
+
+template <int N, bool OUT> constexpr int tensors(const Batch<N, OUT>&) { return N; }
+
+// The tensor that has tile t: as many end before it.
+template <int N, bool OUT>
+__device__ __forceinline__ int tensor_of(const Batch<N, OUT>& b, uint32_t t) {
+  int n = 0;
 #pragma unroll
-  for (int u = 0; u < kTileUnits; ++u) {
-    const int j = threadIdx.x + u * kThreads;
-    if (j * kU < len) add_squares<DT>(acc, t[u], unit_cut<kOddRows>(j, len));
+  for (int i = 0; i < N; i += 64) {
+    const int k = i + threadIdx.x % 64;
+    n += __builtin_popcountll(__ballot(k < N && b.first[min(k, N - 1) + 1] <= t));
+  }
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Tile t of tensor i.
+struct Tile {
+  int64_t at;       // its first element
+  int len, kind;
+};
+template <int N, bool OUT>
+__device__ __forceinline__ Tile tile_of(const Batch<N, OUT>& b, int i, uint32_t t) {
+  const int last = b.last[i];
+  return {(int64_t)(t - b.first[i]) * kTile, t + 1 == b.first[i + 1] ? (last & (kHalf - 1)) + 1 : kTile, last & ~(kHalf - 1)};
+}
+
+// The lane's share of a tile of `len` >= N elements at x: all its loads go out before the first is used.
+// (Lanes behind the end read what the last one does, and own none of it.)
+template <int DT, int N, bool NT>
+__device__ __forceinline__ void load_tile(typename Word<DT, N>::R* t, const void* x, int len) {
+#pragma unroll
+  for (int u = 0; u < kTile / kThreads / N; ++u) {
+    t[u] = load_word<DT, N, NT>(x, own_of<N>(threadIdx.x + u * kThreads, len).at);
   }
 }
 
-// A workgroup takes a run of tiles, whichever tensors they are of.
-__global__ __launch_bounds__(kThreads) void k_squares(TensorBatch b, double* part) {
+template <int DT, bool NT>
+__device__ __forceinline__ void tile_squares(double* acc, const void* p, const Tile& tile) {
+  constexpr int N = DT == 1 ? 4 : 8;
+  const char* x = static_cast<const char*>(p) + tile.at * ElemSize<DT>::value;
+  const int len = tile.len;
+  if (len < N) {
+    const double g = (int)threadIdx.x < len ? (double)load_one<DT>(x, threadIdx.x) : 0.0;
+    acc[0] = __builtin_fma(g, g, acc[0]);
+    return;
+  }
+  typename Word<DT, N>::R t[kTile / kThreads / N];
+  load_tile<DT, N, NT>(t, x, len);
+#pragma unroll
+  for (int u = 0; u < kTile / kThreads / N; ++u) {
+    if (len == kTile) add_squares<N>(acc, values<DT, N>(t[u]), 0);
+    else add_squares<N>(acc, values<DT, N>(t[u]), own_of<N>(threadIdx.x + u * kThreads, len).lo);
+  }
+}
+
+// Workgroups take the tiles in turn, whichever tensors they are of, so that all of them
+// together go through the tensors from front to back.
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_squares(Read b, double* part) {
   __shared__ double lds[kThreads / 64];
-  uint32_t t, hi;
-  tile_range(b.first[kBatchTensors], &t, &hi);
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  for (int i = tensor_of(b, t); t < hi; ++t) {
+  uint32_t t = blockIdx.x;
+  for (int i = tensor_of(b, t); t < b.first[tensors(b)]; t += gridDim.x) {
     while (t >= b.first[i + 1]) ++i;
-    const int64_t at = (int64_t)(t - b.first[i]) * kTile;
-    const int len = (int)min((int64_t)kTile, b.count[i] - at);
-    const int type = b.type[i] & 15;
-    const char* x = static_cast<const char*>(b.in[i]) + at * (type == 1 ? 4 : 2);
-    if (type == 1) tile_squares<1>(acc, x, len);
-    else if (type == 2) tile_squares<2>(acc, x, len);
-    else tile_squares<3>(acc, x, len);
+    const Tile tile = tile_of(b, i, t);
+    if (tile.kind & kFull) tile_squares<1, NT>(acc, b.in[i], tile);
+    else if (tile.kind & kHalf) tile_squares<3, NT>(acc, b.in[i], tile);
+    else tile_squares<2, NT>(acc, b.in[i], tile);
   }
   const double sum = block_sum64((acc[0] + acc[1]) + (acc[2] + acc[3]), lds);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-template <int DT, int OUT>
-__device__ __forceinline__ void tile_scale(const void* x, void* y, int len, const Factor& c) {
-  Unit<DT> t[kTileUnits];
-  load_tile<DT>(t, x, len);
+template <int DT, int OUT, bool NT>
+__device__ __forceinline__ void tile_scale(const void* from, void* to, const Tile& tile, const Factor& c) {
+  constexpr int N = DT == 1 || OUT == 1 ? 4 : 8;
+  const char* x = static_cast<const char*>(from) + tile.at * ElemSize<DT>::value;
+  char* y = static_cast<char*>(to) + tile.at * ElemSize<OUT>::value;
+  const int len = tile.len;
+  if (len < N) {
+    if ((int)threadIdx.x < len) store_one<OUT>(y, threadIdx.x, times(load_one<DT>(x, threadIdx.x), c));
+    return;
+  }
+  typename Word<DT, N>::R t[kTile / kThreads / N];
+  load_tile<DT, N, NT>(t, x, len);
 #pragma unroll
-  for (int u = 0; u < kTileUnits; ++u) {
-    const int j = threadIdx.x + u * kThreads;
-    if (j * kU < len) {
-      float v[kU];
+  for (int u = 0; u < kTile / kThreads / N; ++u) {
+    const Own o = own_of<N>(threadIdx.x + u * kThreads, len);
+    if (o.lo >= N) continue;
+    Some<N> s = values<DT, N>(t[u]);
 #pragma unroll
-      for (int k = 0; k < kU; ++k) v[k] = times(unit_get<DT>(t[u], k), c);
-      store_cut<OUT, kOddRows>(y, 0, unit_cut<kOddRows>(j, len), unit_make<OUT>(v));
-    }
+    for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
+    store_own<OUT, N, NT>(y, 0, o, word_of<OUT, N>(s));
   }
 }
 
-// A factor of one leaves what is scaled in place as it is.
-__global__ __launch_bounds__(kThreads) void k_scale(TensorBatch b, ClipRule r) {
+// A factor of one leaves what is scaled in place as it is.  From the last tile to the first:
+// what the pass before read last may still be cached.
+template <bool NT>
+__global__ __launch_bounds__(kThreads) void k_scale(Scale b, ClipRule r) {
   __shared__ double lds[kThreads / 64];
   const Factor c = factor(r, lds);
-  uint32_t t, hi;
-  tile_range(b.first[kBatchTensors], &t, &hi);
-  for (int i = tensor_of(b, t); t < hi; ++t) {
-    while (t >= b.first[i + 1]) ++i;
-    if (is_one(c) && b.in[i] == b.out[i]) continue;
-    const int64_t at = (int64_t)(t - b.first[i]) * kTile;
-    const int len = (int)min((int64_t)kTile, b.count[i] - at);
-    const int type = b.type[i] & 15, out = b.type[i] >> 4;
-    const char* x = static_cast<const char*>(b.in[i]) + at * (type == 1 ? 4 : 2);
-    char* y = static_cast<char*>(b.out[i]) + at * (out == 1 ? 4 : 2);
-    if (type == 1) tile_scale<1, 1>(x, y, len, c);
-    else if (type == 2 && out == 2) tile_scale<2, 2>(x, y, len, c);
-    else if (type == 2) tile_scale<2, 1>(x, y, len, c);
-    else if (out == 3) tile_scale<3, 3>(x, y, len, c);
-    else tile_scale<3, 1>(x, y, len, c);
+  uint32_t n = b.first[tensors(b)] - blockIdx.x;      // tiles from the first to the workgroup's next
+  for (int i = tensor_of(b, n - 1);; n -= gridDim.x) {
+    while (n - 1 < b.first[i]) --i;
+    if (!is_one(c) || b.in[i] != b.out[i]) {
+      const Tile tile = tile_of(b, i, n - 1);
+      if (tile.kind & kFull) tile_scale<1, 1, NT>(b.in[i], b.out[i], tile, c);
+      else if (tile.kind == 0) tile_scale<2, 2, NT>(b.in[i], b.out[i], tile, c);
+      else if (tile.kind == kWiden) tile_scale<2, 1, NT>(b.in[i], b.out[i], tile, c);
+      else if (tile.kind == kHalf) tile_scale<3, 3, NT>(b.in[i], b.out[i], tile, c);
+      else tile_scale<3, 1, NT>(b.in[i], b.out[i], tile, c);
+    }
+    if (n <= gridDim.x) return;
   }
 }
 
 // ---------------------------------------------------------------- ranks
 
-constexpr int kFoldTile = kThreads * kU;
+// A workgroup's tile: kRuns<NT> times what its lanes move at a time.
+template <int DT> constexpr int kLane = DT == 1 ? 4 : 8;
+template <bool NT> constexpr int kRuns = NT ? 2 : 1;
+template <int DT, bool NT> constexpr int kFoldTile = kThreads * kLane<DT> * kRuns<NT>;
 
-// The sum (mean) over the ranks, rounded to the buffers' type, into `to`, and the
-// squares of what was rounded.  `to` may be one of the buffers: a unit is read from all of them
-// by the thread that writes it.
-template <int DT, int AC>
+// The sum over the ranks, in rank order from 0, of each of the lane's runs; up to eight ranks'
+// loads are in flight together.
+template <int DT, int N, int RUNS, bool NT>
+__device__ __forceinline__ void fold_words(Some<N>* s, const RankPtrs& P, int p, int64_t at, const Own* o) {
+  constexpr int kBatch = 8;
+#pragma unroll
+  for (int u = 0; u < RUNS; ++u) s[u] = Some<N>{};
+  auto add = [&](int u, const typename Word<DT, N>::R w) {
+    const Some<N> v = values<DT, N>(w);
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[u].x[k] += v.x[k];
+  };
+  int r = 0;
+  for (; r + kBatch <= p; r += kBatch) {
+    typename Word<DT, N>::R t[kBatch][RUNS];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < RUNS; ++u) t[b][u] = load_word<DT, N, NT>(P.b[r + b], at + o[u].at);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < RUNS; ++u) add(u, t[b][u]);
+  }
+  for (; r + 2 <= p; r += 2) {
+    typename Word<DT, N>::R t[2][RUNS];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int u = 0; u < RUNS; ++u) t[b][u] = load_word<DT, N, NT>(P.b[r + b], at + o[u].at);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int u = 0; u < RUNS; ++u) add(u, t[b][u]);
+  }
+  if (r < p) {
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) add(u, load_word<DT, N, NT>(P.b[r], at + o[u].at));
+  }
+}
+
+// The sum (mean) over the ranks, rounded to the buffers' type, into the first output, and the
+// squares of what was rounded.  An output may be one of the buffers: an element is read from all of
+// them by the thread that writes it.  The sum is written to the caches, for the next pass.
+template <int DT, bool NT>
 __global__ __launch_bounds__(kThreads) void k_fold_squares(FoldArgs a, double* part) {
+  constexpr int N = kLane<DT>, RUNS = kRuns<NT>, kTile = kFoldTile<DT, NT>;
   __shared__ double lds[kThreads / 64];
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  const int64_t step = (int64_t)gridDim.x * kFoldTile;
-  for (int64_t at = (int64_t)blockIdx.x * kFoldTile; at < a.n; at += step) {
-    const int len = (int)min((int64_t)kFoldTile, a.n - at), j = threadIdx.x;
-    if (j * kU >= len) continue;
-    const Cut cut = unit_cut<AC>(j, len);
-    float x[kU];
-    fold_ranks<DT, AC>(x, a.in, a.p, at, cut);
-    if (a.mean) {
-#pragma unroll
-      for (int k = 0; k < kU; ++k) x[k] = x[k] / (float)a.p;
+  const int64_t step = (int64_t)gridDim.x * kTile;
+  for (int64_t at = (int64_t)blockIdx.x * kTile; at < a.n; at += step) {
+    const int len = (int)min((int64_t)kTile, a.n - at);
+    if (len < N) {
+      if ((int)threadIdx.x >= len) continue;
+      float x = 0.0f;
+      for (int r = 0; r < a.p; ++r) x += load_one<DT>(a.in.b[r], at + threadIdx.x);
+      if (a.mean) x = x / (float)a.p;
+      store_one<DT>(a.out.b[0], at + threadIdx.x, x);
+      const double g = value_of<DT>(one_of<DT>(x));
+      acc[0] = __builtin_fma(g, g, acc[0]);
+      continue;
     }
-    const Unit<DT> t = unit_make<DT>(x);
-    store_cut<DT, AC>(a.out.b[0], at, cut, t);
+    Own o[RUNS];
+    Some<N> s[RUNS];
 #pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      const double g = owns<AC>(cut, k) ? (double)unit_get<DT>(t, k) : 0.0;
-      acc[k % 4] = __builtin_fma(g, g, acc[k % 4]);
+    for (int u = 0; u < RUNS; ++u) o[u] = own_of<N>(threadIdx.x + u * kThreads, len);
+    fold_words<DT, N, RUNS, NT>(s, a.in, a.p, at, o);
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+      if (o[u].lo >= N) continue;
+      if (a.mean) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[u].x[k] = s[u].x[k] / (float)a.p;
+      }
+      const typename Word<DT, N>::R w = word_of<DT, N>(s[u]);
+      store_own<DT, N, false>(a.out.b[0], at, o[u], w);
+      add_squares<N>(acc, values<DT, N>(w), o[u].lo);
     }
   }
   const double sum = block_sum64((acc[0] + acc[1]) + (acc[2] + acc[3]), lds);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// What k_fold_squares left in the first output, times the factor, to all of them.
-template <int DT, int AC>
+// What k_fold_squares left in the first output, times the factor, to all of them; from the last
+// tile to the first, since what was written last is still cached.
+template <int DT, bool NT>
 __global__ __launch_bounds__(kThreads) void k_spread(FoldArgs a, ClipRule r) {
+  constexpr int N = kLane<DT>, kTile = kThreads * N;
   __shared__ double lds[kThreads / 64];
-  const Factor c = factor(r, lds);
-  const int64_t step = (int64_t)gridDim.x * kFoldTile;
-  for (int64_t at = (int64_t)blockIdx.x * kFoldTile; at < a.n; at += step) {
-    const int len = (int)min((int64_t)kFoldTile, a.n - at), j = threadIdx.x;
-    if (j * kU >= len) continue;
-    const Cut cut = unit_cut<AC>(j, len);
-    const Unit<DT> t = load_cut<DT, AC>(a.out.b[0], at, cut);
-    float v[kU];
+  const int64_t last = (a.n + kTile - 1) / kTile - 1 - blockIdx.x;
+  Factor c;
+  for (int64_t t = last; t >= 0; t -= gridDim.x) {
+    const int64_t at = t * kTile;
+    const int len = (int)min((int64_t)kTile, a.n - at);
+    if (len < N) {            // the very last tile: the workgroup's first
+      c = factor(r, lds);
+      if ((int)threadIdx.x >= len) continue;
+      const float x = times(load_one<DT>(a.out.b[0], at + threadIdx.x), c);
+      for (int q = 0; q < a.n_out; ++q) store_one<DT>(a.out.b[q], at + threadIdx.x, x);
+      continue;
+    }
+    const Own o = own_of<N>(threadIdx.x, len);
+    const typename Word<DT, N>::R w = load_word<DT, N, false>(a.out.b[0], at + o.at);
+    if (t == last) c = factor(r, lds);     // while the first load is under way
+    if (o.lo >= N) continue;
+    Some<N> s = values<DT, N>(w);
 #pragma unroll
-    for (int k = 0; k < kU; ++k) v[k] = times(unit_get<DT>(t, k), c);
-    const Unit<DT> y = unit_make<DT>(v);
-    for (int o = 0; o < a.n_out; ++o) store_cut<DT, AC>(a.out.b[o], at, cut, y);
+    for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
+    const typename Word<DT, N>::R y = word_of<DT, N>(s);
+    for (int q = 0; q < a.n_out; ++q) store_own<DT, N, NT>(a.out.b[q], at, o, y);
   }
 }
+
+// ---------------------------------------------------------------- launches
 
 // More parts than this are summed once, by a launch of their own, and not by every
 // workgroup that needs the factor.
 constexpr int kPartsMost = 2048;
+
+// Workgroups of a pass over a batch of tensors, and of the first pass over the ranks' buffers.
+// Constants, so that the order of the sums does not depend on the GPU.
+constexpr int kListGrid = 1024;
+constexpr int kFoldGrid = 1 << 18;
 
 // Where k_finish leaves the factor: in front of the parts.
 float* factor_at(void* work) { return static_cast<float*>(work); }
@@ -261,28 +475,26 @@ hipError_t rule_for(ClipRule* r, void* work, hipStream_t s) {
   return e;
 }
 
-unsigned batch_grid(const TensorBatch& b) { return std::min<uint32_t>(b.first[kBatchTensors], kSquaresGrid); }
-
-// Runs `go` on the tensors [from, to) of a list, as many of them at a time as a launch takes.
-template <typename F>
-hipError_t each_batch(const TensorListArgs& a, int64_t from, int64_t to, F go) {
-  TensorBatch b;
-  while (from < to) {
+// Runs go(batch, workgroups) on the first n tensors of a list, as many of them at a time as a launch takes.
+template <int N, bool OUT, typename F>
+hipError_t each_batch(const TensorListArgs& a, int64_t n, F go) {
+  Batch<N, OUT> b;
+  for (int64_t i = 0; i < n;) {
     uint32_t tiles = 0;
-    int n = 0;
-    for (; n < kBatchTensors && from < to; ++from) {
-      const int64_t count = a.counts[from];
+    int m = 0;
+    for (; m < N && i < n; ++i) {
+      const int64_t count = a.counts[i];
       if (count == 0) continue;
-      b.in[n] = a.in[from];
-      b.out[n] = a.out ? a.out[from] : nullptr;
-      b.count[n] = count;
-      b.type[n] = (uint8_t)(a.types[from] | (a.out_types ? a.out_types[from] : a.types[from]) << 4);
-      b.first[n++] = tiles;
+      const int type = a.types[i], out = OUT && a.out_types ? a.out_types[i] : type;
+      b.in[m] = a.in[i];
+      if (OUT) b.out[m] = a.out[i];
+      b.last[m] = (uint16_t)((count - 1) % kTile | (type == 1 ? kFull : type == 3 ? kHalf : 0) | (out != type ? kWiden : 0));
+      b.first[m++] = tiles;
       tiles += (uint32_t)((count + kTile - 1) / kTile);
     }
-    for (int i = n; i <= kBatchTensors; ++i) b.first[i] = tiles;
-    if (n == 0) break;
-    hipError_t e = go(b);
+    if (m == 0) break;
+    for (; m <= N; ++m) b.first[m] = tiles;
+    hipError_t e = go(b, std::min<uint32_t>(tiles, kListGrid));
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -291,9 +503,9 @@ hipError_t each_batch(const TensorListArgs& a, int64_t from, int64_t to, F go) {
 // The squares' parts; their number goes to *parts.
 hipError_t squares(const TensorListArgs& a, void* work, int* parts, hipStream_t s) {
   int n = 0;
-  hipError_t e = each_batch(a, 0, a.counted, [&](const TensorBatch& b) {
-    const unsigned grid = batch_grid(b);
-    k_squares<<<grid, kThreads, 0, s>>>(b, parts_at(work) + n);
+  hipError_t e = each_batch<256, false>(a, a.counted, [&](const Read& b, unsigned grid) {
+    if (a.stream) k_squares<true><<<grid, kThreads, 0, s>>>(b, parts_at(work) + n);
+    else k_squares<false><<<grid, kThreads, 0, s>>>(b, parts_at(work) + n);
     n += (int)grid;
     return hipGetLastError();
   });
@@ -301,37 +513,38 @@ hipError_t squares(const TensorListArgs& a, void* work, int* parts, hipStream_t 
   return e;
 }
 
-template <int DT, int AC>
+template <int DT, bool NT>
 hipError_t fold_go(const FoldArgs& a, ClipRule r, void* work, hipStream_t s) {
-  const int64_t tiles = (a.n + kFoldTile - 1) / kFoldTile;
-  r.parts = (int)fold_clip_parts(a.n);
+  const int64_t tiles = (a.n + kFoldTile<DT, NT> - 1) / kFoldTile<DT, NT>;
+  const int64_t spread = (a.n + kThreads * kLane<DT> - 1) / (kThreads * kLane<DT>);
+  r.parts = (int)std::min<int64_t>(tiles, kFoldGrid);
   r.part = parts_at(work);
-  k_fold_squares<DT, AC><<<(unsigned)r.parts, kThreads, 0, s>>>(a, parts_at(work));
+  k_fold_squares<DT, NT><<<(unsigned)r.parts, kThreads, 0, s>>>(a, parts_at(work));
   hipError_t e = hipGetLastError();
   if (e == hipSuccess) e = rule_for(&r, work, s);
   if (e != hipSuccess) return e;
-  k_spread<DT, AC><<<(unsigned)std::min<int64_t>(tiles, kMaxGrid), kThreads, 0, s>>>(a, r);
+  k_spread<DT, NT><<<(unsigned)std::min<int64_t>(spread, kMaxGrid), kThreads, 0, s>>>(a, r);
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t fold_access(const FoldArgs& a, const ClipRule& r, int access, void* work, hipStream_t s) {
-  if (access == kStreamRows) return fold_go<DT, kStreamRows>(a, r, work, s);
-  if (access == kAlignedRows) return fold_go<DT, kAlignedRows>(a, r, work, s);
-  return fold_go<DT, kOddRows>(a, r, work, s);
+hipError_t fold_access(const FoldArgs& a, const ClipRule& r, bool stream, void* work, hipStream_t s) {
+  return stream ? fold_go<DT, true>(a, r, work, s) : fold_go<DT, false>(a, r, work, s);
 }
 
 }  // namespace
 
 int64_t grad_norm_bytes(int64_t n) {
-  const int64_t batches = (n + kBatchTensors - 1) / kBatchTensors;
-  return 16 + batches * kSquaresGrid * (int64_t)sizeof(double);
+  const int64_t batches = (n + tensors(Read{}) - 1) / tensors(Read{});
+  return 16 + batches * kListGrid * (int64_t)sizeof(double);
 }
 
-// One part for each of the first pass's workgroups, which take tiles in a stride where there
-// are more.
-int64_t fold_clip_parts(int64_t n) { return std::min<int64_t>((n + kFoldTile - 1) / kFoldTile, kFoldGrid); }
-int64_t fold_clip_bytes(int64_t n) { return 16 + fold_clip_parts(n) * (int64_t)sizeof(double); }
+// A part for each of the first pass's workgroups (float32's tiles are the smallest), which take tiles
+// in a stride where there are more of them.
+int64_t fold_clip_bytes(int64_t n) {
+  constexpr int kLeast = kFoldTile<1, false>;
+  return 16 + std::min<int64_t>((n + kLeast - 1) / kLeast, kFoldGrid) * (int64_t)sizeof(double);
+}
 
 hipError_t launch_grad_norm(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s) {
   hipError_t e = squares(a, work, &r.parts, s);
@@ -345,25 +558,26 @@ hipError_t launch_grad_clip(const TensorListArgs& a, ClipRule r, void* work, hip
   if (e == hipSuccess) e = rule_for(&r, work, s);
   if (e != hipSuccess) return e;
   bool any = false;
-  e = each_batch(a, 0, a.n, [&](const TensorBatch& b) {
+  e = each_batch<176, true>(a, a.n, [&](const Scale& b, unsigned grid) {
     any = true;
-    k_scale<<<batch_grid(b), kThreads, 0, s>>>(b, r);
+    if (a.stream) k_scale<true><<<grid, kThreads, 0, s>>>(b, r);
+    else k_scale<false><<<grid, kThreads, 0, s>>>(b, r);
     return hipGetLastError();
   });
   // without an element to scale, the norm of none
   return e != hipSuccess || any ? e : finish(r, nullptr, s);
 }
 
-hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, int access, void* work, hipStream_t s) {
+hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, bool stream, void* work, hipStream_t s) {
   if (a.n == 0) {
     ClipRule none = r;
     none.parts = 0;
     none.part = nullptr;
     return finish(none, nullptr, s);
   }
-  if (dtype == 1) return fold_access<1>(a, r, access, work, s);
-  if (dtype == 2) return fold_access<2>(a, r, access, work, s);
-  return fold_access<3>(a, r, access, work, s);
+  if (dtype == 1) return fold_access<1>(a, r, stream, work, s);
+  if (dtype == 2) return fold_access<2>(a, r, stream, work, s);
+  return fold_access<3>(a, r, stream, work, s);
 }
 
 }  // namespace ra

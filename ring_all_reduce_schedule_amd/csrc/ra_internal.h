@@ -233,16 +233,6 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, int dtype, int table_dtype, b
 
 // ---------------------------------------------------------------- gradients
 
-// Tensors of one launch; with the launch's other arguments they stay under 4 KiB.
-constexpr int kBatchTensors = 128;
-struct TensorBatch {
-  const void* in[kBatchTensors];
-  void* out[kBatchTensors];
-  int64_t count[kBatchTensors];
-  uint32_t first[kBatchTensors + 1];    // tiles before each tensor's; from the last one on, all tiles
-  uint8_t type[kBatchTensors];          // of what is read, and 16 times that of what is written
-};
-
 // A caller's list.
 struct TensorListArgs {
   const void* const* in;
@@ -251,6 +241,7 @@ struct TensorListArgs {
   const int* types;
   const int* out_types;      // null: the same
   int64_t n, counted;        // the first `counted` make the norm
+  bool stream;               // larger than the caches
 };
 
 // How a norm and a factor come from the sum of squares.
@@ -268,17 +259,11 @@ struct FoldArgs {
   int32_t p, n_out, mean;
 };
 
-// Workgroups of a pass over a batch of tensors, of the first pass over the ranks' buffers.
-// Constants, so that the order of the sums does not depend on the GPU.
-constexpr int kSquaresGrid = 2048;
-constexpr int kFoldGrid = 32768;
-
 int64_t grad_norm_bytes(int64_t n);        // of workspace, for n tensors
-int64_t fold_clip_parts(int64_t n);
 int64_t fold_clip_bytes(int64_t n);        // ... for n elements
 hipError_t launch_grad_norm(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s);
 hipError_t launch_grad_clip(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s);
-hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, int access, void* work, hipStream_t s);
+hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, bool stream, void* work, hipStream_t s);
 
 // ---------------------------------------------------------------- errors
 // Sets the calling thread's error message and returns `code` (ra_api.cpp).

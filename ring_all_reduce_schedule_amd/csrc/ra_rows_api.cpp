@@ -275,7 +275,7 @@ int check_list_length(int64_t n) {
 
 // A list of tensors of any sizes, read, and (outs) what is written for each: the tensor itself or
 // another array.  Neither may share memory with another one that is written.
-int check_list(const ra::TensorListArgs& a, float* norm, void* workspace, int64_t have) {
+int check_list(ra::TensorListArgs& a, float* norm, void* workspace, int64_t have) {
   int rc = RA_OK;
   if (a.n > 0 && (!a.in || !a.counts || !a.types)) return fail(RA_ERR_INVALID_ARG, "tensors, counts or dtypes is NULL");
   const int64_t need = ra::grad_norm_bytes(a.n);
@@ -284,7 +284,7 @@ int check_list(const ra::TensorListArgs& a, float* norm, void* workspace, int64_
   // host memory, for the call alone
   std::unique_ptr<Span[]> list(new (std::nothrow) Span[2 * a.n + 2]);
   if (!list) return fail(RA_ERR_UNSUPPORTED, "no host memory for %lld tensors", (long long)a.n);
-  int64_t m = 0, elements = 0;
+  int64_t m = 0, elements = 0, bytes = 0;
   auto add = [&](const char* what, int64_t i, const void* ptr, int64_t bytes, int elem, bool write) {
     if (!ptr) return fail(RA_ERR_INVALID_ARG, "%s[%lld] is NULL", what, (long long)i);
     const uintptr_t at = reinterpret_cast<uintptr_t>(ptr);
@@ -309,7 +309,9 @@ int check_list(const ra::TensorListArgs& a, float* norm, void* workspace, int64_
     rc = add("tensors", i, a.in[i], count * e, e, same);
     if (rc == RA_OK && a.out && !same) rc = add("outs", i, a.out[i], count * eo, eo, true);
     if (rc != RA_OK) return rc;
+    bytes += count * (e + (a.out ? eo : 0));
   }
+  a.stream = bytes > ra::kStreamingBytes;
   rc = add("norm", 0, norm, 4, 4, true);
   if (rc == RA_OK) rc = add("workspace", 0, workspace, need, 16, true);
   return rc == RA_OK ? check_spans(list.get(), m) : rc;
@@ -700,7 +702,7 @@ int ra_grad_norm(const void* const* tensors, const int64_t* counts, const int* d
                  float* norm, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   int rc = check_list_length(n);
   if (rc == RA_OK) rc = check_positive("scale", scale);
-  ra::TensorListArgs a = {tensors, nullptr, counts, dtypes, nullptr, n, n};
+  ra::TensorListArgs a = {tensors, nullptr, counts, dtypes, nullptr, n, n, false};
   if (rc == RA_OK) rc = check_list(a, norm, workspace, workspace_bytes);
   if (rc != RA_OK) return rc;
   debug_rows("grad_norm", 1, n, 0, n > 0 ? dtypes[0] : 0, false, 1);
@@ -714,7 +716,7 @@ int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes,
   if (rc == RA_OK && (counted < 0 || counted > n))
     rc = fail(RA_ERR_INVALID_ARG, "counted = %lld, need 0..n = %lld", (long long)counted, (long long)n);
   if (rc == RA_OK) rc = check_clip(max_norm, scale);
-  ra::TensorListArgs a = {tensors, outs ? outs : tensors, counts, dtypes, outs ? out_dtypes : nullptr, n, counted};
+  ra::TensorListArgs a = {tensors, outs ? outs : tensors, counts, dtypes, outs ? out_dtypes : nullptr, n, counted, false};
   if (rc == RA_OK) rc = check_list(a, norm, workspace, workspace_bytes);
   if (rc != RA_OK) return rc;
   debug_rows("grad_clip", 1, n, 0, n > 0 ? dtypes[0] : 0, false, 1);
@@ -756,7 +758,6 @@ int ra_allreduce_clip(void* const* bufs, int p, int64_t n, int dtype, int op, fl
       a.out.b[r] = outs[r];
     }
   }
-  const bool al = all.al() && n % 8 == 0;
   if (rc == RA_OK) rc = all.add("norm", -1, norm, 4, 4, true);
   if (rc == RA_OK) rc = check_workspace(&all, workspace, workspace_bytes, ra::fold_clip_bytes(n));
   if (rc == RA_OK) rc = all.overlaps();
@@ -765,9 +766,9 @@ int ra_allreduce_clip(void* const* bufs, int p, int64_t n, int dtype, int op, fl
   a.p = p;
   a.n_out = n_out;
   a.mean = op == RA_AVG;
-  debug_rows("allreduce_clip", p, n, 1, dtype, al, 1);
+  debug_rows("allreduce_clip", p, n, 1, dtype, false, 1);
   return launched(ra::launch_fold_clip(a, dtype, {nullptr, nullptr, norm, 0, max_norm, scale},
-                                       access_of(al, n * e * (p + n_out)), workspace, stream));
+                                       n * e * (p + n_out) > ra::kStreamingBytes, workspace, stream));
 }
 
 }  // extern "C"

@@ -86,7 +86,7 @@ def address(a):
     return a.buffer_info()[0]
 
 
-WS = 16 + 16384
+WS = 16 + 8192
 
 
 def grad_call(name, sizes=(1000, 0, 7), codes=(F32, BF16, F16), ptrs=None, **kw):
@@ -137,13 +137,13 @@ def test_clip_refusals(change, code):
 
 
 def test_list_sizes():
-    assert B.ra_grad_norm_workspace(0) == 16 and B.ra_grad_norm_workspace(1) == B.ra_grad_norm_workspace(128) == WS
-    assert B.ra_grad_norm_workspace(129) == 16 + 2 * 16384
+    assert B.ra_grad_norm_workspace(0) == 16 and B.ra_grad_norm_workspace(1) == B.ra_grad_norm_workspace(256) == WS
+    assert B.ra_grad_norm_workspace(257) == 16 + 2 * 8192
     for bad in (-1, (1 << 20) + 1):
         with pytest.raises(B.RaError):
             B.ra_grad_norm_workspace(bad)
     f = B.ra_allreduce_clip_workspace
-    assert f(0) == 16 and f(1) == f(2048) == 24 and f(2049) == 32 and f(1 << 44) == 16 + 8 * 32768
+    assert f(0) == 16 and f(1) == f(1024) == 24 and f(1025) == 32 and f(1 << 44) == 16 + 8 * 262144
     for bad in (-1, (1 << 44) + 1):
         with pytest.raises(B.RaError):
             f(bad)
