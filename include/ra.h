@@ -609,7 +609,7 @@ int ra_embedding_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidde
  * ra_grad_norm -- norm = scale sqrt(sum of g^2 over every element of n tensors)
  *   tensors, counts, dtypes  host arrays, read during the call only: addresses, elements
  *            and types, which may differ from tensor to tensor.  An empty tensor's address
- *            may be NULL.  At most 2^20 tensors, and 2^44 elements in all.
+ *            may be NULL.  At most 2^20 tensors, and 2^40 elements in all.
  *   scale    > 0 and finite: what the gradients are to be multiplied with (1 / the loss's
  *            scale, 1 / the number of batches)
  *   norm     one float32.  n = 0: 0.
@@ -643,7 +643,7 @@ int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes,
  *     g = sum_r bufs[r]  (RA_AVG: that divided by p), rounded to `dtype`
  *     norm = scale sqrt(sum g^2),   c = scale min(1, max_norm / (norm + 1e-6)),   out = g c
  * The ranks' buffers are added in rank order, 0 first, in float32.
- *   bufs   p arrays of n elements of `dtype` (n up to 2^44)
+ *   bufs   p arrays of n elements of `dtype` (n up to 2^40)
  *   op     RA_SUM or RA_AVG
  *   outs   n_out (1..p) arrays like bufs; each may be one of bufs
  *   norm, max_norm, scale  as above

@@ -195,25 +195,38 @@ __device__ __forceinline__ void add_squares(double* acc, const Some<N>& s, int l
 
 // ---------------------------------------------------------------- many tensors
 
-constexpr int kTile = kThreads * 32;       // elements that a workgroup takes of a tensor at a time
-
-// The tensors of a launch, whose arguments have to stay under 4 KiB: cut into tiles, which
-// go one tensor's behind the other's.
+// The tensors of a launch, cut into tiles, which go one tensor's behind the other's.  A launch's
+// arguments have to stay within 4 KiB, with the 256 bytes that the compiler adds of its own (the
+// grid's size among them).
 template <int N, bool OUT> struct Batch {
   const void* in[N];
   void* out[OUT ? N : 1];
   uint32_t first[N + 1];    // tiles before each tensor's; from the last one on, all tiles
-  uint16_t last[N];         // elements of a tensor's last tile, less 1, and its Kind
+  // Elements of a tensor's last tile, less 1, and its Kind.  32 bits, of which 16 would do: where an
+  // index counts by 2 bytes in one array and by 4 in another, the compiler shares sums of it between
+  // their addresses and splits one into parts that are no multiples of 4, of which a scalar load
+  // drops the low bits.
+  uint32_t last[N];
 };
-typedef Batch<256, false> Read;
-typedef Batch<176, true> Scale;
+typedef Batch<232, false> Read;
+typedef Batch<156, true> Scale;
 enum Kind { kHalf = 1 << 13, kFull = 1 << 14, kWiden = 1 << 15 };   // float16 (neither: bfloat16), float32; out is float32
-static_assert(kTile <= kHalf, "a last tile's elements have 13 bits");
-static_assert(sizeof(Read) + sizeof(ClipRule) + 16 <= 4096 && sizeof(Scale) + sizeof(ClipRule) + 16 <= 4096, "arguments");
+constexpr int kArgsMost = 4096 - 256;
+static_assert(sizeof(Read) + sizeof(double*) <= kArgsMost && sizeof(Scale) + sizeof(ClipRule) <= kArgsMost, "arguments");
 
 template <int N, bool OUT> constexpr int tensors(const Batch<N, OUT>&) { return N; }
 
-// The tensor that has tile t: as many end before it.
+// Elements of a tile: what the norm reads has 32 for each thread, all of them under way together.
+// The pass that scales has one access of each thread: read and written streams go best that way
+// (2.4 GB into 2.4 GB: 742 us, two accesses 820, four 833), in workgroups that take a tile each
+// (884 in ones that stay).
+constexpr int kReadTile = kThreads * 32;
+__host__ __device__ constexpr int scale_tile(int kind) { return kThreads * (kind & (kFull | kWiden) ? 4 : 8); }
+template <bool OUT> __host__ __device__ constexpr int tile_elements(int kind) { return OUT ? scale_tile(kind) : kReadTile; }
+static_assert(kReadTile <= kHalf, "a last tile's elements have 13 bits");
+
+// The tensor that has tile t: as many end before it.  One round trip for the whole list, which in a
+// small launch no cache holds yet.  The whole wave has to be active.
 template <int N, bool OUT>
 __device__ __forceinline__ int tensor_of(const Batch<N, OUT>& b, uint32_t t) {
   int n = 0;
@@ -225,6 +238,17 @@ __device__ __forceinline__ int tensor_of(const Batch<N, OUT>& b, uint32_t t) {
   return __builtin_amdgcn_readfirstlane(n);
 }
 
+// The same by halving: eight scalar loads, one behind the other, from the scalar cache.  For launches
+// of many workgroups that look up one tile each (2.4 GB into 2.4 GB: 800 us).
+template <int N, bool OUT>
+__device__ __forceinline__ int tensor_by_halving(const Batch<N, OUT>& b, uint32_t t) {
+  int lo = 0;
+#pragma unroll
+  for (int step = 128; step > 0; step /= 2)
+    if (lo + step < N && b.first[lo + step] <= t) lo += step;
+  return lo;
+}
+
 // Tile t of tensor i.
 struct Tile {
   int64_t at;       // its first element
@@ -232,18 +256,8 @@ struct Tile {
 };
 template <int N, bool OUT>
 __device__ __forceinline__ Tile tile_of(const Batch<N, OUT>& b, int i, uint32_t t) {
-  const int last = b.last[i];
-  return {(int64_t)(t - b.first[i]) * kTile, t + 1 == b.first[i + 1] ? (last & (kHalf - 1)) + 1 : kTile, last & ~(kHalf - 1)};
-}
-
-// The lane's share of a tile of `len` >= N elements at x: all its loads go out before the first is used.
-// (Lanes behind the end read what the last one does, and own none of it.)
-template <int DT, int N, bool NT>
-__device__ __forceinline__ void load_tile(typename Word<DT, N>::R* t, const void* x, int len) {
-#pragma unroll
-  for (int u = 0; u < kTile / kThreads / N; ++u) {
-    t[u] = load_word<DT, N, NT>(x, own_of<N>(threadIdx.x + u * kThreads, len).at);
-  }
+  const int last = (int)b.last[i], kind = last & ~(kHalf - 1), all = tile_elements<OUT>(kind);
+  return {(int64_t)(t - b.first[i]) * all, t + 1 == b.first[i + 1] ? (last & (kHalf - 1)) + 1 : all, kind};
 }
 
 template <int DT, bool NT>
@@ -256,11 +270,15 @@ __device__ __forceinline__ void tile_squares(double* acc, const void* p, const T
     acc[0] = __builtin_fma(g, g, acc[0]);
     return;
   }
-  typename Word<DT, N>::R t[kTile / kThreads / N];
-  load_tile<DT, N, NT>(t, x, len);
+  // All loads go out before the first is used.  Lanes behind the end read what the last one does, and
+  // own none of it.
+  constexpr int kLoads = kReadTile / kThreads / N;
+  typename Word<DT, N>::R t[kLoads];
 #pragma unroll
-  for (int u = 0; u < kTile / kThreads / N; ++u) {
-    if (len == kTile) add_squares<N>(acc, values<DT, N>(t[u]), 0);
+  for (int u = 0; u < kLoads; ++u) t[u] = load_word<DT, N, NT>(x, own_of<N>(threadIdx.x + u * kThreads, len).at);
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    if (len == kReadTile) add_squares<N>(acc, values<DT, N>(t[u]), 0);
     else add_squares<N>(acc, values<DT, N>(t[u]), own_of<N>(threadIdx.x + u * kThreads, len).lo);
   }
 }
@@ -293,17 +311,13 @@ __device__ __forceinline__ void tile_scale(const void* from, void* to, const Til
     if ((int)threadIdx.x < len) store_one<OUT>(y, threadIdx.x, times(load_one<DT>(x, threadIdx.x), c));
     return;
   }
-  typename Word<DT, N>::R t[kTile / kThreads / N];
-  load_tile<DT, N, NT>(t, x, len);
+  const Own o = own_of<N>(threadIdx.x, len);
+  const typename Word<DT, N>::R w = load_word<DT, N, NT>(x, o.at);
+  if (o.lo >= N) return;
+  Some<N> s = values<DT, N>(w);
 #pragma unroll
-  for (int u = 0; u < kTile / kThreads / N; ++u) {
-    const Own o = own_of<N>(threadIdx.x + u * kThreads, len);
-    if (o.lo >= N) continue;
-    Some<N> s = values<DT, N>(t[u]);
-#pragma unroll
-    for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
-    store_own<OUT, N, NT>(y, 0, o, word_of<OUT, N>(s));
-  }
+  for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
+  store_own<OUT, N, NT>(y, 0, o, word_of<OUT, N>(s));
 }
 
 // A factor of one leaves what is scaled in place as it is.  From the last tile to the first:
@@ -312,8 +326,8 @@ template <bool NT>
 __global__ __launch_bounds__(kThreads) void k_scale(Scale b, ClipRule r) {
   __shared__ double lds[kThreads / 64];
   const Factor c = factor(r, lds);
-  uint32_t n = b.first[tensors(b)] - blockIdx.x;      // tiles from the first to the workgroup's next
-  for (int i = tensor_of(b, n - 1);; n -= gridDim.x) {
+  uint32_t n = b.first[tensors(b)] - blockIdx.x;           // tiles up to the workgroup's
+  for (int i = NT ? tensor_by_halving(b, n - 1) : tensor_of(b, n - 1);; n -= gridDim.x) {
     while (n - 1 < b.first[i]) --i;
     if (!is_one(c) || b.in[i] != b.out[i]) {
       const Tile tile = tile_of(b, i, n - 1);
@@ -449,13 +463,10 @@ __global__ __launch_bounds__(kThreads) void k_spread(FoldArgs a, ClipRule r) {
 
 // ---------------------------------------------------------------- launches
 
-// More parts than this are summed once, by a launch of their own, and not by every
-// workgroup that needs the factor.
-constexpr int kPartsMost = 2048;
-
-// Workgroups of a pass over a batch of tensors, and of the first pass over the ranks' buffers.
-// Constants, so that the order of the sums does not depend on the GPU.
+// Workgroups of the pass over a batch of tensors that sums, and of the first pass over the ranks'
+// buffers.  Constants, so that the order of the sums does not depend on the GPU.
 constexpr int kListGrid = 1024;
+constexpr unsigned kScaleGrid = 2048;     // of the pass that scales, where the caches serve it
 constexpr int kFoldGrid = 1 << 18;
 
 // Where k_finish leaves the factor: in front of the parts.
@@ -467,15 +478,26 @@ hipError_t finish(const ClipRule& r, float* to, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts or the factor, for the kernel that scales.
-hipError_t rule_for(ClipRule* r, void* work, hipStream_t s) {
-  if (r->parts <= kPartsMost) return hipSuccess;
+// Parts or the factor, for the kernels that scale: few parts are summed by every one of few workgroups,
+// more by a launch of their own.
+constexpr int64_t kSumMost = 2048;
+hipError_t rule_for(ClipRule* r, int64_t workgroups, void* work, hipStream_t s) {
+  if (r->parts <= kSumMost && workgroups <= kSumMost) return hipSuccess;
   hipError_t e = finish(*r, factor_at(work), s);
   r->factor = factor_at(work);
   return e;
 }
 
-// Runs go(batch, workgroups) on the first n tensors of a list, as many of them at a time as a launch takes.
+// The tiles of a tensor.
+template <bool OUT>
+int64_t tiles_of(const TensorListArgs& a, int64_t i, int* kind) {
+  const int type = a.types[i], out = OUT && a.out_types ? a.out_types[i] : type;
+  *kind = (type == 1 ? kFull : type == 3 ? kHalf : 0) | (out != type ? kWiden : 0);
+  const int all = tile_elements<OUT>(*kind);
+  return (a.counts[i] + all - 1) / all;
+}
+
+// Runs go(batch, tiles) on the first n tensors of a list, as many of them at a time as a launch takes.
 template <int N, bool OUT, typename F>
 hipError_t each_batch(const TensorListArgs& a, int64_t n, F go) {
   Batch<N, OUT> b;
@@ -483,18 +505,18 @@ hipError_t each_batch(const TensorListArgs& a, int64_t n, F go) {
     uint32_t tiles = 0;
     int m = 0;
     for (; m < N && i < n; ++i) {
-      const int64_t count = a.counts[i];
-      if (count == 0) continue;
-      const int type = a.types[i], out = OUT && a.out_types ? a.out_types[i] : type;
+      if (a.counts[i] == 0) continue;
+      int kind;
+      const int64_t mine = tiles_of<OUT>(a, i, &kind);
       b.in[m] = a.in[i];
       if (OUT) b.out[m] = a.out[i];
-      b.last[m] = (uint16_t)((count - 1) % kTile | (type == 1 ? kFull : type == 3 ? kHalf : 0) | (out != type ? kWiden : 0));
+      b.last[m] = (uint32_t)((a.counts[i] - 1) % tile_elements<OUT>(kind) | kind);
       b.first[m++] = tiles;
-      tiles += (uint32_t)((count + kTile - 1) / kTile);
+      tiles += (uint32_t)mine;
     }
     if (m == 0) break;
     for (; m <= N; ++m) b.first[m] = tiles;
-    hipError_t e = go(b, std::min<uint32_t>(tiles, kListGrid));
+    hipError_t e = go(b, tiles);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -503,7 +525,8 @@ hipError_t each_batch(const TensorListArgs& a, int64_t n, F go) {
 // The squares' parts; their number goes to *parts.
 hipError_t squares(const TensorListArgs& a, void* work, int* parts, hipStream_t s) {
   int n = 0;
-  hipError_t e = each_batch<256, false>(a, a.counted, [&](const Read& b, unsigned grid) {
+  hipError_t e = each_batch<232, false>(a, a.counted, [&](const Read& b, uint32_t tiles) {
+    const unsigned grid = std::min<unsigned>(tiles, kListGrid);
     if (a.stream) k_squares<true><<<grid, kThreads, 0, s>>>(b, parts_at(work) + n);
     else k_squares<false><<<grid, kThreads, 0, s>>>(b, parts_at(work) + n);
     n += (int)grid;
@@ -521,7 +544,7 @@ hipError_t fold_go(const FoldArgs& a, ClipRule r, void* work, hipStream_t s) {
   r.part = parts_at(work);
   k_fold_squares<DT, NT><<<(unsigned)r.parts, kThreads, 0, s>>>(a, parts_at(work));
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess) e = rule_for(&r, work, s);
+  if (e == hipSuccess) e = rule_for(&r, spread, work, s);
   if (e != hipSuccess) return e;
   k_spread<DT, NT><<<(unsigned)std::min<int64_t>(spread, kMaxGrid), kThreads, 0, s>>>(a, r);
   return hipGetLastError();
@@ -555,17 +578,18 @@ hipError_t launch_grad_norm(const TensorListArgs& a, ClipRule r, void* work, hip
 hipError_t launch_grad_clip(const TensorListArgs& a, ClipRule r, void* work, hipStream_t s) {
   hipError_t e = squares(a, work, &r.parts, s);
   r.part = parts_at(work);
-  if (e == hipSuccess) e = rule_for(&r, work, s);
-  if (e != hipSuccess) return e;
-  bool any = false;
-  e = each_batch<176, true>(a, a.n, [&](const Scale& b, unsigned grid) {
-    any = true;
-    if (a.stream) k_scale<true><<<grid, kThreads, 0, s>>>(b, r);
-    else k_scale<false><<<grid, kThreads, 0, s>>>(b, r);
-    return hipGetLastError();
-  });
+  int64_t tiles = 0;
+  int kind;
+  for (int64_t i = 0; i < a.n; ++i) tiles += tiles_of<true>(a, i, &kind);
+  if (e == hipSuccess) e = rule_for(&r, a.stream ? tiles : kScaleGrid, work, s);
+  if (e == hipSuccess)
+    e = each_batch<156, true>(a, a.n, [&](const Scale& b, uint32_t tiles) {
+      if (a.stream) k_scale<true><<<std::min<uint32_t>(tiles, kMaxGrid), kThreads, 0, s>>>(b, r);
+      else k_scale<false><<<std::min<uint32_t>(tiles, kScaleGrid), kThreads, 0, s>>>(b, r);
+      return hipGetLastError();
+    });
   // without an element to scale, the norm of none
-  return e != hipSuccess || any ? e : finish(r, nullptr, s);
+  return e != hipSuccess || tiles > 0 ? e : finish(r, nullptr, s);
 }
 
 hipError_t launch_fold_clip(const FoldArgs& a, int dtype, const ClipRule& r, bool stream, void* work, hipStream_t s) {

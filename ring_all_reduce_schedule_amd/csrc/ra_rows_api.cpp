@@ -258,11 +258,11 @@ int check_clip(float max_norm, float scale) {
 }
 
 // Tensors of one call, and elements of them all: workgroups and their parts are counted in 32 bits.
-constexpr int64_t kListMost = 1 << 20, kListElements = 1ll << 44;
+constexpr int64_t kListMost = 1 << 20, kListElements = 1ll << 40;
 
 int check_elements(int64_t n) {
   if (n < 0) return fail(RA_ERR_INVALID_ARG, "n = %lld, need n >= 0", (long long)n);
-  if (n > kListElements) return fail(RA_ERR_UNSUPPORTED, "n = %lld, at most 2^44 elements", (long long)n);
+  if (n > kListElements) return fail(RA_ERR_UNSUPPORTED, "n = %lld, at most 2^40 elements", (long long)n);
   return RA_OK;
 }
 
@@ -298,7 +298,7 @@ int check_list(ra::TensorListArgs& a, float* norm, void* workspace, int64_t have
     const int64_t count = a.counts[i];
     if (count < 0) return fail(RA_ERR_INVALID_ARG, "counts[%lld] = %lld", (long long)i, (long long)count);
     if (count > kListElements || (elements += count) > kListElements)
-      return fail(RA_ERR_UNSUPPORTED, "more than 2^44 elements in a call");
+      return fail(RA_ERR_UNSUPPORTED, "more than 2^40 elements in a call");
     rc = check_real("dtype", a.types[i]);
     if (rc == RA_OK && a.out && a.out_types) rc = check_second("out_dtype", a.out_types[i], a.types[i]);
     if (rc != RA_OK) return rc;

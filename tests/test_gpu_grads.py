@@ -81,6 +81,13 @@ def test_clip(sizes, types, off, how, part):
     untouched(norm)
 
 
+@pytest.mark.parametrize("types,off", [(["bf16"], 0), (["bf16", "f16"], 1), (["f32"], 1)])
+@pytest.mark.parametrize("how", ["in place", "outs", "wide"])
+def test_lists_larger_than_the_caches(types, off, how):
+    """More than 512 MiB, whose accesses go past the caches."""
+    test_clip([(1 << 27) + 3, 5, 1 << 20, (1 << 27) + 9, 2], types, off, how, 0.5)
+
+
 def test_a_factor_of_one_changes_no_bit():
     require_gpu()
     g = gradients([1000, 5, 8192 * 3 + 1], ["bf16", "f32", "f16"], 5)
