@@ -216,13 +216,16 @@ static_assert(sizeof(Read) + sizeof(double*) <= kArgsMost && sizeof(Scale) + siz
 
 template <int N, bool OUT> constexpr int tensors(const Batch<N, OUT>&) { return N; }
 
-// Elements of a tile: what the norm reads has 32 for each thread, all of them under way together.
-// The pass that scales has one access of each thread: read and written streams go best that way
-// (2.4 GB into 2.4 GB: 742 us, two accesses 820, four 833), in workgroups that take a tile each
-// (884 in ones that stay).
+// Accesses of a thread to a tile.  What the norm reads: 32 elements, all under way together.  The pass
+// that scales beyond the caches has one access: read and written streams go best that way (2.4 GB into
+// 2.4 GB: 742 us, two accesses 820, four 833), in workgroups that take a tile each (884 in ones that stay).
+// Where the caches serve it, four, in workgroups that stay (33 MB into 66 MB: 22 us, one access 27).
+template <bool NT> constexpr int kScaleLoads = NT ? 1 : 4;
 constexpr int kReadTile = kThreads * 32;
-__host__ __device__ constexpr int scale_tile(int kind) { return kThreads * (kind & (kFull | kWiden) ? 4 : 8); }
-template <bool OUT> __host__ __device__ constexpr int tile_elements(int kind) { return OUT ? scale_tile(kind) : kReadTile; }
+template <bool OUT>
+__host__ __device__ constexpr int tile_elements(int kind, bool stream) {
+  return OUT ? kThreads * (stream ? kScaleLoads<true> : kScaleLoads<false>) * (kind & (kFull | kWiden) ? 4 : 8) : kReadTile;
+}
 static_assert(kReadTile <= kHalf, "a last tile's elements have 13 bits");
 
 // The tensor that has tile t: as many end before it.  One round trip for the whole list, which in a
@@ -254,9 +257,9 @@ struct Tile {
   int64_t at;       // its first element
   int len, kind;
 };
-template <int N, bool OUT>
+template <bool NT, int N, bool OUT>
 __device__ __forceinline__ Tile tile_of(const Batch<N, OUT>& b, int i, uint32_t t) {
-  const int last = (int)b.last[i], kind = last & ~(kHalf - 1), all = tile_elements<OUT>(kind);
+  const int last = (int)b.last[i], kind = last & ~(kHalf - 1), all = tile_elements<OUT>(kind, NT);
   return {(int64_t)(t - b.first[i]) * all, t + 1 == b.first[i + 1] ? (last & (kHalf - 1)) + 1 : all, kind};
 }
 
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(kThreads) void k_squares(Read b, double* part) {
   uint32_t t = blockIdx.x;
   for (int i = tensor_of(b, t); t < b.first[tensors(b)]; t += gridDim.x) {
     while (t >= b.first[i + 1]) ++i;
-    const Tile tile = tile_of(b, i, t);
+    const Tile tile = tile_of<NT>(b, i, t);
     if (tile.kind & kFull) tile_squares<1, NT>(acc, b.in[i], tile);
     else if (tile.kind & kHalf) tile_squares<3, NT>(acc, b.in[i], tile);
     else tile_squares<2, NT>(acc, b.in[i], tile);
@@ -311,13 +314,18 @@ __device__ __forceinline__ void tile_scale(const void* from, void* to, const Til
     if ((int)threadIdx.x < len) store_one<OUT>(y, threadIdx.x, times(load_one<DT>(x, threadIdx.x), c));
     return;
   }
-  const Own o = own_of<N>(threadIdx.x, len);
-  const typename Word<DT, N>::R w = load_word<DT, N, NT>(x, o.at);
-  if (o.lo >= N) return;
-  Some<N> s = values<DT, N>(w);
+  typename Word<DT, N>::R w[kScaleLoads<NT>];
 #pragma unroll
-  for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
-  store_own<OUT, N, NT>(y, 0, o, word_of<OUT, N>(s));
+  for (int u = 0; u < kScaleLoads<NT>; ++u) w[u] = load_word<DT, N, NT>(x, own_of<N>(threadIdx.x + u * kThreads, len).at);
+#pragma unroll
+  for (int u = 0; u < kScaleLoads<NT>; ++u) {
+    const Own o = own_of<N>(threadIdx.x + u * kThreads, len);
+    if (o.lo >= N) continue;
+    Some<N> s = values<DT, N>(w[u]);
+#pragma unroll
+    for (int k = 0; k < N; ++k) s.x[k] = times(s.x[k], c);
+    store_own<OUT, N, NT>(y, 0, o, word_of<OUT, N>(s));
+  }
 }
 
 // A factor of one leaves what is scaled in place as it is.  From the last tile to the first:
@@ -330,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void k_scale(Scale b, ClipRule r) {
   for (int i = NT ? tensor_by_halving(b, n - 1) : tensor_of(b, n - 1);; n -= gridDim.x) {
     while (n - 1 < b.first[i]) --i;
     if (!is_one(c) || b.in[i] != b.out[i]) {
-      const Tile tile = tile_of(b, i, n - 1);
+      const Tile tile = tile_of<NT>(b, i, n - 1);
       if (tile.kind & kFull) tile_scale<1, 1, NT>(b.in[i], b.out[i], tile, c);
       else if (tile.kind == 0) tile_scale<2, 2, NT>(b.in[i], b.out[i], tile, c);
       else if (tile.kind == kWiden) tile_scale<2, 1, NT>(b.in[i], b.out[i], tile, c);
@@ -493,7 +501,7 @@ template <bool OUT>
 int64_t tiles_of(const TensorListArgs& a, int64_t i, int* kind) {
   const int type = a.types[i], out = OUT && a.out_types ? a.out_types[i] : type;
   *kind = (type == 1 ? kFull : type == 3 ? kHalf : 0) | (out != type ? kWiden : 0);
-  const int all = tile_elements<OUT>(*kind);
+  const int all = tile_elements<OUT>(*kind, a.stream);
   return (a.counts[i] + all - 1) / all;
 }
 
@@ -510,7 +518,7 @@ hipError_t each_batch(const TensorListArgs& a, int64_t n, F go) {
       const int64_t mine = tiles_of<OUT>(a, i, &kind);
       b.in[m] = a.in[i];
       if (OUT) b.out[m] = a.out[i];
-      b.last[m] = (uint32_t)((a.counts[i] - 1) % tile_elements<OUT>(kind) | kind);
+      b.last[m] = (uint32_t)((a.counts[i] - 1) % tile_elements<OUT>(kind, a.stream) | kind);
       b.first[m++] = tiles;
       tiles += (uint32_t)mine;
     }
