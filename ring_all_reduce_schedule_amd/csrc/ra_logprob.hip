@@ -38,8 +38,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return a;
 }
 
-// Joins a unit; `top` becomes the largest of itself and the unit's logits.  NaN is passed over
-// by the maxima, and makes z NaN.
+// Joins a unit; `top` becomes the largest of itself and the unit's logits.  m and c are the wave's: after
+// a row's first units a larger m is rare, and c costs a comparison.  NaN is passed over by the maxima,
+// and makes z NaN.
 template <int DT>
 __device__ __forceinline__ void take(Stat& t, float& top, const Unit<DT>& u, float s2) {
   float x[kU];
@@ -47,15 +48,16 @@ __device__ __forceinline__ void take(Stat& t, float& top, const Unit<DT>& u, flo
   for (int i = 0; i < kU; ++i) x[i] = unit_get<DT>(u, i);
   const float most = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), -INFINITY);
   top = __builtin_fmaxf(top, most);
-  t.m = __builtin_fmaxf(t.m, most);
-  const float c = __builtin_fmaxf(kNone, t.m * s2);
-  const float d = t.c - c, r = exp2_of(d);
-  t.w = r * __builtin_fmaf(d, t.z, t.w);
-  t.z *= r;
-  t.c = c;
+  if (__any(most > t.m)) {
+    t.m = wave_max(__builtin_fmaxf(most, t.m));
+    const float c = __builtin_fmaxf(kNone, t.m * s2), d = t.c - c, r = exp2_of(d);
+    t.w = r * __builtin_fmaf(d, t.z, t.w);
+    t.z *= r;
+    t.c = c;
+  }
 #pragma unroll
   for (int i = 0; i < kU; ++i) {
-    const float y = __builtin_fmaf(x[i], s2, -c), e = exp2_of(y);
+    const float y = __builtin_fmaf(x[i], s2, -t.c), e = exp2_of(y);
     t.z += e;
     t.w = __builtin_fmaf(e, __builtin_fmaxf(y, kFloor), t.w);
   }
@@ -96,23 +98,21 @@ __device__ __forceinline__ bool settle(Stat& t, float s2) {
   return good;
 }
 
-// The chunks of a workgroup: [lo, hi), its waves taking one each in turn.
+// The chunks of a workgroup: lo, lo + step, ... below hi, its waves taking one each in turn.  The parts of
+// a row take turns, too: the last chunks, which are short where pieces end in them, go to many.
 struct Range {
-  int lo, hi;
+  int lo, hi, step;
 };
-__device__ __forceinline__ Range range_of(const VocabArgs& a, int part) {
-  const int per = (a.total + a.splits - 1) / a.splits, lo = min(a.total, part * per);
-  return {lo, min(a.total, lo + per)};
-}
+__device__ __forceinline__ Range range_of(const VocabArgs& a, int part) { return {part, a.total, a.splits}; }
 
 // The statistics of a range with the largest logit subtracted first, by the workgroup.
 template <int DT, int MODE>
 __device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range g, float s2, float* lds) {
   const int w = wave_id(), waves = blockDim.x / 64;
   float m = -INFINITY;
-  for (int q = g.lo + w; q < g.hi; q += waves) {
+  for (int q = g.lo + w * g.step; q < g.hi; q += waves * g.step) {
     Unit<DT> u[1];
-    fetch_all<DT, MODE, 1>(u, a, row, q, waves, g.hi);
+    fetch_all<DT, MODE, 1>(u, a, row, q, waves * g.step, g.hi);
 #pragma unroll
     for (int i = 0; i < kU; ++i) m = __builtin_fmaxf(m, unit_get<DT>(u[0], i));
   }
@@ -124,9 +124,9 @@ __device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range
   __syncthreads();
   const float at = m == -INFINITY ? 0.0f : m;
   float z = 0.0f, v = 0.0f;
-  for (int q = g.lo + w; q < g.hi; q += waves) {
+  for (int q = g.lo + w * g.step; q < g.hi; q += waves * g.step) {
     Unit<DT> u[1];
-    fetch_all<DT, MODE, 1>(u, a, row, q, waves, g.hi);
+    fetch_all<DT, MODE, 1>(u, a, row, q, waves * g.step, g.hi);
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       const float y = (unit_get<DT>(u[0], i) - at) * s2, e = exp2_of(y);
@@ -155,82 +155,75 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 // ... with the column, of which lower ones come first.
 __device__ __forceinline__ uint64_t place_of(uint32_t key, int col) { return (uint64_t)key << 32 | ~(uint32_t)col; }
 
-constexpr int kCap = 1024;      // columns that are put in order
-constexpr int kSlack = 32;      // a bound that this many more threads reach than have to will do
+constexpr int kCap = 1024;      // columns that are kept
+constexpr int kOrder = 256;     // ... and that are put in order as they are; of more, kFew at most
+constexpr int kFew = 128;
+constexpr int kWork = 512;      // groups that are read again at once
+constexpr int kSets = 128;      // threads are taken together in so many sets for the bound
+// A bound that so many more sets or columns reach than have to will do.
+__device__ __forceinline__ int slack(int k) { return 4 + k / 4; }
 
-struct Pick {
+template <int G> struct Pick {
   uint64_t best[kCap];
+  uint32_t lanes[G];
+  union {
+    uint16_t work[kWork];
+    uint64_t few[kFew];
+  };
+  uint64_t from;
   uint32_t bound;
-  int n, sum[2];
+  int n, groups, sum[2];
 };
 
-// Runs f(place) on the elements of the thread's groups whose maximum reaches `key`.
+// Runs f(place) on the elements of a unit that count.
+template <int DT, typename F>
+__device__ __forceinline__ void each_of(const LogpArgs& a, const Chunk& s, const Lane& l, const Unit<DT>& u, F f) {
+#pragma unroll
+  for (int i = 0; i < kU; ++i)
+    if (counts(s, l, a.valid, i)) f(place_of(order_of(unit_get<DT>(u, i)), s.col0 - s.c0 + l.c + i));
+}
+
+// Runs f(place) on the elements of the thread's groups whose maximum reaches `key`.  `top`: the largest
+// order of every group, as the threads read them.
 template <int DT, int MODE, typename F>
 __device__ __forceinline__ void each_in(const LogpArgs& a, int64_t row, Range g, const uint32_t* top, uint32_t key,
                                         F f) {
-  const int waves = blockDim.x / 64;
-  for (int q0 = g.lo + wave_id(), b = 0; q0 < g.hi; q0 += kMore * waves, ++b) {
+  const int waves = blockDim.x / 64, next = waves * g.step;
+  for (int q0 = g.lo + wave_id() * g.step, b = 0; q0 < g.hi; q0 += kMore * waves * g.step, ++b) {
     if (top[b * blockDim.x + threadIdx.x] < key) continue;
     Unit<DT> u[kMore];
 #pragma unroll
-    for (int k = 0; k < kMore; ++k) u[k] = fetch<DT, MODE>(a, row, chunk(a, min(q0 + k * waves, g.hi - 1)));
+    for (int k = 0; k < kMore; ++k) u[k] = fetch<DT, MODE>(a, row, chunk(a, min(q0 + k * next, g.hi - 1)));
 #pragma unroll
     for (int k = 0; k < kMore; ++k) {
-      if (q0 + k * waves >= g.hi) continue;
-      const Chunk s = chunk(a, q0 + k * waves);
-      const Lane l = lane_of<MODE>(s);
-#pragma unroll
-      for (int i = 0; i < kU; ++i)
-        if (counts(s, l, a.valid, i)) f(place_of(order_of(unit_get<DT>(u[k], i)), s.col0 - s.c0 + l.c + i));
+      if (q0 + k * next >= g.hi) continue;
+      const Chunk s = chunk(a, q0 + k * next);
+      each_of<DT>(a, s, lane_of<MODE>(s), u[k], f);
     }
   }
 }
 
-// Elements of the range at or above a place.
-template <int DT, int MODE>
-__device__ __forceinline__ int count_from(const LogpArgs& a, int64_t row, Range g, const uint32_t* top, Pick* P,
-                                          int turn, uint64_t from) {
-  int n = 0;
-  each_in<DT, MODE>(a, row, g, top, (uint32_t)(from >> 32), [&](uint64_t x) { n += x >= from; });
-  if (threadIdx.x == 0) P->sum[turn] = 0;
-  __syncthreads();
-  atomicAdd(&P->sum[turn], n);
-  __syncthreads();
-  return P->sum[turn];     // zeroed again two calls and a barrier later
+template <int G>
+__device__ __forceinline__ void keep(Pick<G>* P, uint64_t x) {
+  const int i = atomicAdd(&P->n, 1);
+  if (i < kCap) P->best[i] = x;
 }
 
-// Keeps the elements at or above a place, in any order, and returns their number.
-template <int DT, int MODE>
-__device__ __forceinline__ int keep_from(const LogpArgs& a, int64_t row, Range g, const uint32_t* top, Pick* P,
-                                         uint64_t from) {
-  if (threadIdx.x == 0) P->n = 0;
-  __syncthreads();
-  each_in<DT, MODE>(a, row, g, top, (uint32_t)(from >> 32), [&](uint64_t x) {
-    if (x < from) return;
-    const int i = atomicAdd(&P->n, 1);
-    if (i < kCap) P->best[i] = x;
-  });
-  __syncthreads();
-  return P->n;
-}
-
-// The k-th largest of G values, or a smaller one that at most kSlack more reach; by one wave.
+// The k-th largest of the maxima of kSets sets of threads, or a smaller one that at most slack(k) more sets
+// reach; by one wave.  (With a set for each thread, more of the k best are sets' maxima, and the
+// bound is higher; 128 sets bring 22 of the row's elements for 20, 89 for 64, in a quarter of the
+// steps.)
 template <int G>
 __device__ __forceinline__ uint32_t bound_of(const uint32_t* v, int k) {
-  uint32_t x[G / 64], least = 0xffffffffu, most = 0;
+  const int lane = threadIdx.x % 64;
+  uint32_t x = 0, y = 0;
 #pragma unroll
-  for (int i = 0; i < G / 64; ++i) {
-    x[i] = v[i * 64 + threadIdx.x % 64];
-    least = min(least, x[i]);
-    most = max(most, x[i]);
+  for (int i = 0; i < G; i += kSets) {
+    x = max(x, v[i + lane]);
+    y = max(y, v[i + 64 + lane]);
   }
-  auto reach = [&](uint32_t at) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < G / 64; ++i) n += __builtin_popcountll(__ballot(x[i] >= at));
-    return n;
-  };
-  uint32_t hi = wave_max_u32(most), lo = ~wave_max_u32(~least);
+  auto reach = [&](uint32_t at) { return __builtin_popcountll(__ballot(x >= at)) + __builtin_popcountll(__ballot(y >= at)); };
+  uint32_t hi = wave_max_u32(max(x, y)), lo = ~wave_max_u32(~min(x, y));
   if (reach(hi) >= k) return hi;
   while (hi - lo > 1) {            // lo is reached by k at least, hi by fewer
     const uint32_t mid = lo + (hi - lo) / 2;
@@ -239,54 +232,133 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t* v, int k) {
       hi = mid;
     } else {
       lo = mid;
-      if (n <= k + kSlack) break;
+      if (n <= k + slack(k)) break;
     }
   }
   return lo;
 }
 
-// Leaves the k best elements of a range (all, if it has fewer), and a few more perhaps, in P->best and
-// returns how many.  `top`: the largest order of every group, as the threads read them; `lanes`: room
-// for G words.
-template <int DT, int MODE, int G>
-__device__ __forceinline__ int pick(const LogpArgs& a, int64_t row, Range g, int k, const uint32_t* top,
-                                    uint32_t* lanes, Pick* P) {
-  uint32_t mine = 0;
-  const int waves = G / 64;
-  for (int q0 = g.lo + wave_id(), b = 0; q0 < g.hi; q0 += kMore * waves, ++b) mine = max(mine, top[b * G + threadIdx.x]);
-  lanes[threadIdx.x] = mine;
+// A place that at least k of n > k places reach, and at most slack(k) more; all reach lo.  By one wave.
+__device__ __forceinline__ uint64_t place_bound(const uint64_t* v, int n, int k, uint64_t lo) {
+  uint64_t hi = ~0ull;
+  while (hi - lo > 1) {
+    const uint64_t mid = lo + (hi - lo) / 2;
+    int m = 0;
+    for (int i = 0; i < n; i += 64) {
+      const int j = i + threadIdx.x % 64;
+      m += __builtin_popcountll(__ballot(j < n && v[min(j, n - 1)] >= mid));
+    }
+    if (m < k) {
+      hi = mid;
+    } else {
+      lo = mid;
+      if (m <= k + slack(k)) break;
+    }
+  }
+  return lo;
+}
+
+// The k best places that a workgroup's threads have (all, if there are fewer), and a few more perhaps.
+// mine: the largest order that the thread has.  quick(bound): keeps the places whose order reaches the
+// bound, or only counts groups beyond kWork.  each(key, f): runs f(place) on the thread's places, where it may
+// pass over orders below the key.
+struct Picked {
+  const uint64_t* list;
+  int n;
+};
+template <int G, typename Quick, typename Each>
+__device__ __forceinline__ Picked pick(int k, uint32_t mine, Pick<G>* P, Quick quick, Each each) {
+  P->lanes[threadIdx.x] = mine;
+  if (threadIdx.x == 0) P->n = P->groups = 0;
   __syncthreads();
   if (threadIdx.x < 64) {
-    const uint32_t t = bound_of<G>(lanes, k);
+    const uint32_t t = bound_of<G>(P->lanes, k);
     if (threadIdx.x == 0) P->bound = max(t, 1u);
   }
   __syncthreads();
   const uint32_t bound = P->bound;
+  quick(bound);
+  __syncthreads();
   uint64_t lo = (uint64_t)bound << 32;
-  int n = keep_from<DT, MODE>(a, row, g, top, P, lo);
-  if (n <= kCap) return n;
-  // lo is reached by more than k, hi by fewer (or is the last place there is)
-  uint64_t hi = ~0ull, mid = bound == 0xffffffffu ? lo + (1ull << 31) : (uint64_t)(bound + 1) << 32;
-  for (int turn = 0; hi - lo > 1; turn ^= 1, mid = lo + (hi - lo) / 2) {
-    n = count_from<DT, MODE>(a, row, g, top, P, turn, mid);
-    if (n < k) {
-      hi = mid;
-    } else {
-      lo = mid;
-      if (n <= kCap) break;
+  int n = P->groups > kWork ? kCap + 1 : P->n;
+  if (n > kCap) {
+    // ties, or many of the best in few threads.  lo is reached by more than k, hi by fewer (or is the
+    // last place there is)
+    uint64_t hi = ~0ull;
+    uint64_t mid = bound == 0xffffffffu ? lo + (1ull << 31) : (uint64_t)(bound + 1) << 32;
+    for (int turn = 0; hi - lo > 1; turn ^= 1, mid = lo + (hi - lo) / 2) {
+      if (threadIdx.x == 0) P->sum[turn] = 0;
+      __syncthreads();
+      int m = 0;
+      each((uint32_t)(mid >> 32), [&](uint64_t x) { m += x >= mid; });
+      atomicAdd(&P->sum[turn], m);
+      __syncthreads();
+      n = P->sum[turn];         // zeroed again two turns and three barriers later
+      if (n < k) {
+        hi = mid;
+      } else {
+        lo = mid;
+        if (n <= kCap) break;
+      }
     }
+    __syncthreads();
+    if (threadIdx.x == 0) P->n = 0;
+    __syncthreads();
+    each((uint32_t)(lo >> 32), [&](uint64_t x) {
+      if (x >= lo) keep(P, x);
+    });
+    __syncthreads();
+    n = P->n;
+  }
+  if (n <= kOrder) return {P->best, n};
+  if (threadIdx.x < 64) {
+    const uint64_t t = place_bound(P->best, n, k, lo);
+    if (threadIdx.x == 0) P->from = t, P->groups = 0;
   }
   __syncthreads();
-  return keep_from<DT, MODE>(a, row, g, top, P, lo);
+  for (int i = threadIdx.x; i < n; i += G)
+    if (P->best[i] >= P->from) P->few[atomicAdd(&P->groups, 1)] = P->best[i];
+  __syncthreads();
+  return {P->few, P->groups};
 }
 
-// f(rank, place) for the first k of P->best's n.
-template <typename F>
-__device__ __forceinline__ void in_order(const Pick* P, int n, int k, F f) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const uint64_t x = P->best[i];
+// The k best of a row's range.
+template <int DT, int MODE, int G>
+__device__ __forceinline__ Picked pick_row(const LogpArgs& a, int64_t row, Range g, int k, const uint32_t* top,
+                                           Pick<G>* P) {
+  constexpr int waves = G / 64;
+  uint32_t mine = 0;
+  for (int q0 = g.lo + wave_id() * g.step, b = 0; q0 < g.hi; q0 += kMore * waves * g.step, ++b) mine = max(mine, top[b * G + threadIdx.x]);
+  return pick<G>(k, mine, P, [&](uint32_t bound) {
+    // the groups that reach the bound, then a thread to each unit of them: one round trip to memory
+    for (int q0 = g.lo + wave_id() * g.step, b = 0; q0 < g.hi; q0 += kMore * waves * g.step, ++b) {
+      if (top[b * G + threadIdx.x] < bound) continue;
+      const int i = atomicAdd(&P->groups, 1);
+      if (i < kWork) P->work[i] = (uint16_t)(b * G + threadIdx.x);
+    }
+    __syncthreads();
+    const int units = min(P->groups, kWork) * kMore;
+    for (int i = threadIdx.x; i < units; i += G) {
+      const int e = P->work[i / kMore], from = e % G;
+      const int q = g.lo + (from / 64 + (e / G * kMore + i % kMore) * waves) * g.step;
+      if (q >= g.hi) continue;
+      const Chunk s = chunk_of(a, q);
+      const Lane l = lane_of<MODE>(s, from % 64);
+      each_of<DT>(a, s, l, fetch<DT, MODE>(a, row, s, l), [&](uint64_t x) {
+        if (x >> 32 >= bound) keep(P, x);
+      });
+    }
+  }, [&](uint32_t key, auto f) { each_in<DT, MODE>(a, row, g, top, key, f); });
+}
+
+// f(rank, place) for the first k of some places.
+template <int G, typename F>
+__device__ __forceinline__ void in_order(const Picked& t, int k, F f) {
+  for (int i = threadIdx.x; i < t.n; i += G) {
+    const uint64_t x = t.list[i];
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += P->best[j] > x;
+#pragma unroll 4
+    for (int j = 0; j < t.n; ++j) rank += t.list[j] > x;
     if (rank < k) f(rank, x);
   }
 }
@@ -303,18 +375,27 @@ __device__ __forceinline__ float log_p(const Row& t, float x, float scale) {
   return empty(t) ? -INFINITY : (x - t.m) * scale - t.ln_z;
 }
 
-// One thread's work.
+// The given token's logit and its column, or what there is instead: kNoToken, kNoColumn.
+constexpr int kNoToken = -1, kNoColumn = -2;
+struct Given {
+  int col;
+  float x;
+};
 template <int DT>
-__device__ __forceinline__ void write_row(const LogpArgs& a, int64_t row, const Row& t) {
-  if (a.lse) a.lse[row] = empty(t) ? -INFINITY : __builtin_fmaf(t.m, a.scale, t.ln_z);
-  if (a.entropy) a.entropy[row] = empty(t) ? 0.0f : t.ln_z - t.w / t.z * kLn2;
-  if (!a.logprob) return;
+__device__ __forceinline__ Given given(const LogpArgs& a, int64_t row) {
+  if (!a.logprob) return {kNoToken, 0.0f};
   const int64_t id = a.ids64 ? static_cast<const int64_t*>(a.ids)[row]
                              : (int64_t)static_cast<const int32_t*>(a.ids)[row];
-  float r = 0.0f;
-  if (id >= a.valid) r = __uint_as_float(0x7fc00000u);
-  else if (id >= 0) r = log_p(t, logit<DT>(a, row, (int)id), a.scale);
-  a.logprob[row] = r;
+  const int col = id < 0 ? kNoToken : id < a.valid ? (int)id : kNoColumn;
+  return {col, logit<DT>(a, row, col)};
+}
+
+// One thread's work.
+__device__ __forceinline__ void write_row(const LogpArgs& a, int64_t row, const Row& t, const Given& y) {
+  if (a.lse) a.lse[row] = empty(t) ? -INFINITY : __builtin_fmaf(t.m, a.scale, t.ln_z);
+  if (a.entropy) a.entropy[row] = empty(t) ? 0.0f : t.ln_z - t.w / t.z * kLn2;
+  if (a.logprob)
+    a.logprob[row] = y.col == kNoToken ? 0.0f : y.col == kNoColumn ? __uint_as_float(0x7fc00000u) : log_p(t, y.x, a.scale);
 }
 
 __device__ __forceinline__ void write_top(const LogpArgs& a, int64_t row, const Row& t, int rank, uint64_t place) {
@@ -339,18 +420,18 @@ template <int DT, int G, int MODE, bool TOP>
 __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
   extern __shared__ uint32_t top[];        // TOP: for each group of 32 that a thread reads, its maximum's order
   __shared__ Stat stats[16];
-  __shared__ Pick pool;
-  __shared__ uint32_t lanes[TOP ? G : 1];
+  __shared__ Pick<G> pool;
   const int waves = G / 64, w = wave_id();
   const unsigned splits = a.splits;
   const int64_t row = a.row0 + blockIdx.x / splits;
   const int part = blockIdx.x % splits;
   const Range g = range_of(a, part);
   const float s2 = a.scale * kLog2e;
+  const Given y = a.splits > 1 ? Given{kNoToken, 0.0f} : given<DT>(a, row);     // under way with the logits
   Stat t = none();
-  for (int q = g.lo + w, b = 0; q < g.hi; q += kMore * waves, ++b) {
+  for (int q = g.lo + w * g.step, b = 0; q < g.hi; q += kMore * waves * g.step, ++b) {
     Unit<DT> u[kMore];
-    fetch_all<DT, MODE, kMore>(u, a, row, q, waves, g.hi);
+    fetch_all<DT, MODE, kMore>(u, a, row, q, waves * g.step, g.hi);
     float most = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kMore; ++k) take<DT>(t, most, u[k], s2);
@@ -362,9 +443,9 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
     t = plain_stat<DT, MODE>(a, row, g, s2, reinterpret_cast<float*>(stats));
     if (TOP && t.z != t.z) {
       // the maxima passed over NaN, which is the largest
-      for (int q = g.lo + w, b = 0; q < g.hi; q += kMore * waves, ++b) {
+      for (int q = g.lo + w * g.step, b = 0; q < g.hi; q += kMore * waves * g.step, ++b) {
         Unit<DT> u[kMore];
-        fetch_all<DT, MODE, kMore>(u, a, row, q, waves, g.hi);
+        fetch_all<DT, MODE, kMore>(u, a, row, q, waves * g.step, g.hi);
         uint32_t most = 0;
 #pragma unroll
         for (int k = 0; k < kMore; ++k)
@@ -384,57 +465,64 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
     }
     if constexpr (TOP) {
       uint64_t* list = reinterpret_cast<uint64_t*>(to + 4);
-      const int n = pick<DT, MODE, G>(a, row, g, a.top, top, lanes, &pool);
-      for (int i = n + threadIdx.x; i < a.top; i += G) list[i] = 0;
-      in_order(&pool, n, a.top, [&](int rank, uint64_t place) { list[rank] = place; });
+      const Picked best = pick_row<DT, MODE, G>(a, row, g, a.top, top, &pool);
+      for (int i = best.n + threadIdx.x; i < a.top; i += G) list[i] = 0;
+      in_order<G>(best, a.top, [&](int rank, uint64_t place) { list[rank] = place; });
     }
   } else {
-    if (threadIdx.x == 0) write_row<DT>(a, row, r);
+    if (threadIdx.x == 0) write_row(a, row, r, y);
     if constexpr (TOP) {
-      const int n = pick<DT, MODE, G>(a, row, g, a.top, top, lanes, &pool);
-      in_order(&pool, n, a.top, [&](int rank, uint64_t place) { write_top(a, row, r, rank, place); });
+      const Picked best = pick_row<DT, MODE, G>(a, row, g, a.top, top, &pool);
+      in_order<G>(best, a.top, [&](int rank, uint64_t place) { write_top(a, row, r, rank, place); });
     }
   }
 }
 
-// The parts of a row, at most 64: a wave to a row.  Its best columns are the parts' merged:
-// the largest of the parts' first ones, k times.
-template <int DT>
-__global__ __launch_bounds__(64) void k_logp_join(LogpArgs a) {
-  extern __shared__ uint64_t lists[];
+// The parts of a row, at most 64.  Their best columns, at most 64 of each, lie in LDS.
+constexpr int kJoinThreads = 256;
+
+template <int DT, bool TOP>
+__global__ __launch_bounds__(TOP ? kJoinThreads : 64) void k_logp_join(LogpArgs a) {
+  extern __shared__ uint64_t places[];
+  __shared__ Pick<kJoinThreads> pool;
+  constexpr int G = TOP ? kJoinThreads : 64;
   const int64_t row = a.row0 + blockIdx.x;
-  const int lane = threadIdx.x;
-  const float s2 = a.scale * kLog2e;
+  const int lane = threadIdx.x % 64;
+  const float* parts = part_space(a, row * a.splits);
   Stat t = {-INFINITY, 0.0f, 0.0f, 0.0f};
   if (lane < a.splits) {
-    const float* from = part_space(a, row * a.splits + lane);
+    const float* from = parts + lane * (4 + 2 * a.top);
     t = {from[0], 0.0f, from[1], from[2]};
   }
-  const float m = wave_max(t.m);
+  const Given y = given<DT>(a, row);
+  uint32_t mine = 0;
+  const int n = a.splits * a.top;
+  if constexpr (TOP) {
+    for (int i = threadIdx.x; i < n; i += G) {
+      // the parts' first ones first, so that they go to many threads
+      const int k = i / a.splits, part = i - k * a.splits;
+      const uint64_t x = reinterpret_cast<const uint64_t*>(parts + part * (4 + 2 * a.top) + 4)[k];
+      places[i] = x;
+      mine = max(mine, (uint32_t)(x >> 32));
+    }
+  }
+  // every wave for itself
+  const float s2 = a.scale * kLog2e, m = wave_max(t.m);
   // NaN (of -inf - -inf) becomes the floor, too
   const float d = __builtin_fmaxf((t.m - m) * s2, kFloor), r = exp2_of(d);
   const Row all = row_of({m, 0.0f, wave_sum(r * t.z), wave_sum(r * __builtin_fmaf(d, t.z, t.w))});
-  if (lane == 0) write_row<DT>(a, row, all);
-  if (a.top == 0) return;
-  for (int i = lane; i < a.splits * a.top; i += 64) {
-    const int part = i / a.top, k = i % a.top;
-    lists[i] = reinterpret_cast<const uint64_t*>(part_space(a, row * a.splits + part) + 4)[k];
+  if (threadIdx.x == 0) write_row(a, row, all, y);
+  if constexpr (TOP) {
+    auto each = [&](uint32_t, auto f) {
+      for (int i = threadIdx.x; i < n; i += G) f(places[i]);
+    };
+    const Picked best = pick<G>(a.top, mine, &pool, [&](uint32_t bound) {
+      each(bound, [&](uint64_t x) {
+        if (x >> 32 >= bound) keep(&pool, x);
+      });
+    }, each);
+    in_order<G>(best, a.top, [&](int rank, uint64_t place) { write_top(a, row, all, rank, place); });
   }
-  __syncthreads();
-  uint64_t mine = 0;
-  int next = 0;
-  uint64_t head = lane < a.splits ? lists[lane * a.top] : 0;
-  for (int k = 0; k < a.top; ++k) {
-    const uint32_t hi = wave_max_u32((uint32_t)(head >> 32));
-    const uint32_t lo = wave_max_u32((uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
-    const uint64_t best = (uint64_t)hi << 32 | lo;
-    if (lane == k) mine = best;
-    if (head == best) {
-      ++next;
-      head = next < a.top ? lists[lane * a.top + next] : 0;
-    }
-  }
-  if (lane < a.top) write_top(a, row, all, lane, mine);
 }
 
 // The gradient: `splits` workgroups to a row.
@@ -445,7 +533,8 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(LogpArgs a) {
   constexpr int kWaves = kGradThreads / 64;
   const unsigned splits = a.splits;
   const int64_t row = a.row0 + blockIdx.x / splits;
-  const Range g = range_of(a, blockIdx.x % splits);
+  const int per = (a.total + splits - 1) / splits, lo = min(a.total, (int)(blockIdx.x % splits) * per);
+  const int hi = min(a.total, lo + per);
   int64_t id = -1;
   if (a.dlogprob)
     id = a.ids64 ? static_cast<const int64_t*>(a.ids)[row] : (int64_t)static_cast<const int32_t*>(a.ids)[row];
@@ -458,13 +547,13 @@ __global__ __launch_bounds__(kGradThreads) void k_logp_grad(LogpArgs a) {
   const int y = id >= 0 && id < a.valid ? (int)id : -1;
   da *= a.scale;
   db *= a.scale;
-  for (int q0 = g.lo + wave_id(); q0 < g.hi; q0 += kMore * kWaves) {
+  for (int q0 = lo + wave_id(); q0 < hi; q0 += kMore * kWaves) {
     Unit<DT> u[kMore];
-    if (!zero) fetch_all<DT, MODE, kMore>(u, a, row, q0, kWaves, g.hi);
+    if (!zero) fetch_all<DT, MODE, kMore>(u, a, row, q0, kWaves, hi);
 #pragma unroll
     for (int k = 0; k < kMore; ++k) {
       const int q = q0 + k * kWaves;
-      if (q >= g.hi) continue;
+      if (q >= hi) continue;
       const Chunk s = chunk(a, q);
       const Lane l = lane_of<MODE>(s);
       const int col = s.col0 - s.c0 + l.c;
@@ -502,7 +591,8 @@ hipError_t rows_go(const LogpArgs& args, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.splits == 1) continue;
-    k_logp_join<DT><<<(unsigned)rows, 64, lists, s>>>(a);
+    if (a.top > 0) k_logp_join<DT, true><<<(unsigned)rows, kJoinThreads, lists, s>>>(a);
+    else k_logp_join<DT, false><<<(unsigned)rows, 64, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -26,10 +26,7 @@ struct Chunk {
 };
 constexpr int kChunk = 64 * kU;
 
-__device__ __forceinline__ Chunk chunk(const VocabArgs& a, int q) {
-  // Computed where it is used: kept over a row's passes, the places of sixteen
-  // chunks would not fit the scalar registers.
-  asm volatile("" : "+s"(q));
+__device__ __forceinline__ Chunk chunk_of(const VocabArgs& a, int q) {
   Chunk s;
   const int wholes = a.whole * a.p;
   if (q < wholes) {
@@ -42,6 +39,14 @@ __device__ __forceinline__ Chunk chunk(const VocabArgs& a, int q) {
   s.len = piece_len(a.cut, s.r);
   s.col0 = piece_lo(a.cut, s.r) + s.c0;
   return s;
+}
+
+// A wave's chunk.
+__device__ __forceinline__ Chunk chunk(const VocabArgs& a, int q) {
+  // Computed where it is used: kept over a row's passes, the places of sixteen
+  // chunks would not fit the scalar registers.
+  asm volatile("" : "+s"(q));
+  return chunk_of(a, q);
 }
 
 // How a kernel reads and writes units.
@@ -59,11 +64,13 @@ struct Lane {
   int c, from;
 };
 template <int MODE>
-__device__ __forceinline__ Lane lane_of(const Chunk& s) {
-  const int from = s.c0 + (int)(threadIdx.x % 64) * kU;
+__device__ __forceinline__ Lane lane_of(const Chunk& s, int lane) {
+  const int from = s.c0 + lane * kU;
   if (MODE == kTiny) return {from, from};
   return {min(from, s.len - kU), from};
 }
+template <int MODE>
+__device__ __forceinline__ Lane lane_of(const Chunk& s) { return lane_of<MODE>(s, (int)(threadIdx.x % 64)); }
 
 // Which elements count: the lane's own, before the first column that is not valid.
 __device__ __forceinline__ bool counts(const Chunk& s, const Lane& l, int valid, int i) {
@@ -84,14 +91,18 @@ __device__ __forceinline__ void mask_out(Unit<DT>* t, int i) {
 
 // The lane's unit of a chunk as memory holds it.
 template <int DT, int MODE>
-__device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s) {
+__device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s, const Lane& l) {
   const char* x = static_cast<const char*>(a.x.b[s.r]) + row * s.len * ElemSize<DT>::value;
-  const Lane l = lane_of<MODE>(s);
   if constexpr (MODE != kTiny) {
     return load_unit<DT, MODE == kAligned>(x, l.c);
   } else {
     return load_cut<DT, false>(x, 0, {l.c, 0, max(0, min(kU, s.len - l.c))});
   }
+}
+
+template <int DT, int MODE>
+__device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s) {
+  return fetch<DT, MODE>(a, row, s, lane_of<MODE>(s));
 }
 
 // ... with -inf for what does not count: the first a.full chunks count as a whole.
