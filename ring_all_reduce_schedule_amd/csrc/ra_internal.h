@@ -200,8 +200,8 @@ struct LogpArgs : VocabArgs {
 constexpr int kTopMost = 64;   // a lane for each
 int logp_splits(int64_t tokens, int vocab, int p);
 int64_t logp_bytes(int64_t tokens, int splits, int top);
-hipError_t launch_logp(const LogpArgs& a, int dtype, bool al, hipStream_t s);
-hipError_t launch_logp_bwd(const LogpArgs& a, int dtype, bool al, hipStream_t s);
+hipError_t launch_logp(const LogpArgs& a, int dtype, int access, hipStream_t s);
+hipError_t launch_logp_bwd(const LogpArgs& a, int dtype, bool al, bool big, hipStream_t s);   // big: more than the caches hold
 
 struct EmbedArgs {
   RankPtrs table, out;

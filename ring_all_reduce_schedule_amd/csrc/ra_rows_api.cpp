@@ -650,7 +650,7 @@ int ra_token_logprobs(void* const* logits, int p, int64_t tokens, int64_t vocab,
   a.splits = ra::logp_splits(tokens, (int)vocab, p);
   const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
   debug_rows("token_logprobs", p, tokens, vocab, dtype, al, a.splits);
-  return launched(ra::launch_logp(a, dtype, al, stream));
+  return launched(ra::launch_logp(a, dtype, access_of(al, tokens * vocab * ra::elem_bytes(dtype)), stream));
 }
 
 int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
@@ -684,11 +684,9 @@ int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64
   a.dlogprob = dlogprob;
   a.dentropy = dentropy;
   a.scale = scale;
-  // A row is cut so that a wave has about four chunks.
-  a.splits = (int32_t)std::max<int64_t>(1, (int64_t)a.total / 16);
   const bool al = all.al() && a.cut.extra == 0 && a.cut.base % 8 == 0;
-  debug_rows("token_logprobs_backward", p, tokens, vocab, dtype, al, a.splits);
-  return launched(ra::launch_logp_bwd(a, dtype, al, stream));
+  debug_rows("token_logprobs_backward", p, tokens, vocab, dtype, al, 1);
+  return launched(ra::launch_logp_bwd(a, dtype, al, 2 * tokens * vocab * ra::elem_bytes(dtype) > ra::kStreamingBytes, stream));
 }
 
 int ra_grad_norm_workspace(int64_t n, int64_t* bytes) {

@@ -52,9 +52,12 @@ __device__ __forceinline__ Chunk chunk(const VocabArgs& a, int q) {
 // How a kernel reads and writes units.
 enum Mode {
   kAligned,   // rows of whole units on 16-byte boundaries
+  kStream,    // those, past the caches
   kOdd,       // any rows of pieces of at least a unit
   kTiny       // pieces shorter than a unit are among them: element by element
 };
+
+constexpr int access_of(int mode) { return mode == kStream ? kStreamRows : mode == kAligned ? kAlignedRows : kOddRows; }
 
 // The lane's unit of a chunk: it loads elements [c, c + 8) of the piece's row,
 // and its own are those from `from` on that the piece has.  The unit that would
@@ -94,7 +97,7 @@ template <int DT, int MODE>
 __device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s, const Lane& l) {
   const char* x = static_cast<const char*>(a.x.b[s.r]) + row * s.len * ElemSize<DT>::value;
   if constexpr (MODE != kTiny) {
-    return load_unit<DT, MODE == kAligned>(x, l.c);
+    return load_unit<DT, access_of(MODE)>(x, l.c);
   } else {
     return load_cut<DT, false>(x, 0, {l.c, 0, max(0, min(kU, s.len - l.c))});
   }
@@ -161,9 +164,9 @@ template <int DT, int MODE, bool WHOLE>
 __device__ __forceinline__ void put(const VocabArgs& a, int64_t row, const Chunk& s, const Lane& l, const Unit<DT>& t) {
   char* dx = static_cast<char*>(a.dx.b[s.r]) + row * s.len * ElemSize<DT>::value;
   if (WHOLE) {
-    store_unit<DT, MODE == kAligned>(dx, l.from, t);
+    store_unit<DT, access_of(MODE)>(dx, l.from, t);
   } else if (l.from < s.len) {
-    store_cut<DT, MODE == kAligned>(dx, 0, {l.c, l.from - l.c, min(kU, s.len - l.c)}, t);
+    store_cut<DT, access_of(MODE)>(dx, 0, {l.c, l.from - l.c, min(kU, s.len - l.c)}, t);
   }
 }
 
