@@ -1,0 +1,418 @@
+"""The log probabilities and the gradients' norm and clipping as a program uses them: a step of
+training on sampled answers over virtual ranks, captured graphs, streams, workspaces, arrays beyond
+2^32 elements, and refusals with device tensors."""
+
+import math
+
+import pytest
+import torch
+
+from ring_all_reduce_schedule_amd import binding as B
+from tests import answers_ref as A
+from tests import rows_ref as R
+from tests.gpu_util import require_gpu
+from tests.pads import cut
+
+pytestmark = pytest.mark.gpu
+
+P, TOK, HID, VOCAB, TEMP, MAX_NORM = 3, 40, 24, 211, 0.8, 0.05
+
+
+def weights(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [0.3 * torch.randn((VOCAB // P + (r < VOCAB % P), HID), device="cuda", generator=g) for r in range(P)]
+
+
+def batch(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((P, TOK, HID), device="cuda", generator=g)
+    ids = torch.randint(0, VOCAB, (P, TOK), device="cuda", generator=g)
+    ids[:, 3] = -1                                          # a token that is no answer
+    return x, ids, torch.randn((P, TOK), device="cuda", generator=g), torch.randn((P, TOK), device="cuda", generator=g) + 3
+
+
+def library_step(w, x, ids, advantage, old):
+    """Each of P replicas has a batch of its own, and its head's vocabulary is cut over P ranks: a policy loss
+    with clipped ratios and a bonus for entropy, its gradient, and the replicas' gradients averaged and clipped."""
+    f = dict(device="cuda", dtype=torch.float32)
+    flat = []
+    for r in range(P):
+        logits = [x[r] @ h.t() for h in w]
+        lp, ent, lse = (torch.empty(TOK, **f) for _ in range(3))
+        top, ltop = torch.empty((TOK, 4), device="cuda", dtype=torch.int64), torch.empty((TOK, 4), **f)
+        B.ra_token_logprobs(logits, ids[r], lp, ent, lse, top, ltop, scale=1 / TEMP)
+        ratio = torch.exp(lp + old[r])
+        inside = (ratio < 1.2) | (advantage[r] < 0)
+        da = -(ratio * inside * advantage[r]) / TOK
+        B.ra_token_logprobs_backward(logits, ids[r], lse, logits, da, ent, torch.full_like(da, -0.01 / TOK),
+                                     scale=1 / TEMP)        # the gradients take the logits' place
+        flat.append(torch.cat([(g.t() @ x[r]).flatten() for g in logits]))
+    norm = torch.empty(1, **f)
+    B.ra_allreduce_clip(flat, MAX_NORM, norm)
+    # the clipped gradients once more, a tensor a rank's head: their norm is at most MAX_NORM
+    heads = flat[0].split([h.numel() for h in w])
+    again = torch.empty(1, **f)
+    B.ra_grad_norm(list(heads), again)
+    return flat, norm, again, top
+
+
+def exact_step(w, x, ids, advantage, old):
+    w = [h.double().cpu().requires_grad_() for h in w]
+    x, ids, advantage, old = x.double().cpu(), ids.cpu(), advantage.double().cpu(), old.double().cpu()
+    total, tops = 0.0, None
+    for r in range(P):
+        y = x[r] @ torch.cat(w).t()
+        ln_p = torch.log_softmax(y / TEMP, 1)
+        lp = torch.where(ids[r] >= 0, ln_p.gather(1, ids[r].clamp_min(0).unsqueeze(1)).squeeze(1), 0.0)
+        ratio = torch.exp(lp + old[r])
+        inside = (ratio < 1.2) | (advantage[r] < 0)
+        ent = -(ln_p.exp() * ln_p).sum(1)
+        total = total - ((ratio * inside * advantage[r]).sum() + 0.01 * ent.sum()) / TOK
+        tops = y.topk(4).indices
+    (total / P).backward()
+    g = torch.cat([h.grad.flatten() for h in w])
+    return g, g.norm(), tops
+
+
+def compare(got, want):
+    flat, norm, again, top = got
+    g, n, tops = want
+    # float32 chains of some ten products of up to 211 terms: 2^-24 times about 1000 of the norm
+    tol = 1000 * R.U
+    c = min(1.0, MAX_NORM / (float(n) + 1e-6))
+    assert abs(float(norm) - float(n)) <= tol * float(n)
+    assert float(n) > MAX_NORM and abs(float(again) - MAX_NORM) <= tol * MAX_NORM + 1e-6
+    for f in flat:
+        assert float((f.double().cpu() - c * g).norm()) <= tol * c * float(n)
+        assert torch.equal(f, flat[0])
+    assert torch.equal(top.cpu(), tops)
+
+
+def test_training_step_on_sampled_answers():
+    require_gpu()
+    w = weights(1)
+    args = batch(2)
+    compare(library_step(w, *args), exact_step(w, *args))
+
+
+def test_training_step_in_a_graph():
+    """Captured once and replayed on other batches, with eager steps between the replays."""
+    require_gpu()
+    w = weights(3)
+    args = batch(4)
+    library_step(w, *args)                          # the libraries' first calls, outside the capture
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    print("[case] capture of a step on sampled answers", flush=True)
+    with torch.cuda.graph(graph, stream=s):
+        out = library_step(w, *args)
+    for seed in (5, 6, 7):
+        new = batch(seed)
+        for a, b in zip(args, new):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        compare(out, exact_step(w, *args))
+        eager = library_step(w, *new)
+        for a, b in zip(out[0] + list(out[1:]), eager[0] + list(eager[1:])):
+            assert torch.equal(a, b)
+
+
+def scoring(t, v, p, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = (2 * torch.randn((t, v), device="cuda", generator=g)).to(dtype)
+    y = torch.randint(0, v, (t,), device="cuda", generator=g)
+    f = dict(device="cuda", dtype=torch.float32)
+    out = [torch.empty(t, **f) for _ in range(3)] + [torch.empty((t, 20), device="cuda", dtype=torch.int64), torch.empty((t, 20), **f)]
+    return cut(x, p), y, out
+
+
+def test_two_graphs_replayed_side_by_side():
+    """Each graph owns its workspaces: rows shared by workgroups, norms with many parts."""
+    require_gpu()
+    cases, graphs = [], []
+    for k in range(2):
+        x, y, out = scoring(4, 100_000, 4, torch.bfloat16, k)
+        grads = [torch.randn(60_000 + 999 * i, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9 * k + i)) for i in range(30)]
+        outs = [torch.empty_like(g) for g in grads]
+        bufs = [torch.randn(3_000_001, device="cuda", generator=torch.Generator(device="cuda").manual_seed(70 + 9 * k + i)) for i in range(3)]
+        to = [torch.empty_like(b) for b in bufs]
+        norms = torch.empty(2, device="cuda")
+
+        def step(x=x, y=y, out=out, grads=grads, outs=outs, bufs=bufs, to=to, norms=norms):
+            B.ra_token_logprobs(x, y, *out)
+            B.ra_grad_clip(grads, 1.0, norms[:1], outs=outs)
+            B.ra_allreduce_clip(bufs, 1.0, norms[1:], to)
+            return out + outs + to + [norms]
+        want = [t.clone() for t in step()]
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        print(f"[case] capture {k}", flush=True)
+        with torch.cuda.graph(g, stream=s):
+            got = step()
+        cases.append((got, want, step))                # step holds the graph's inputs
+        graphs.append((g, s))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for got, *_ in cases:
+            for t in got:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in graphs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for got, want, _ in cases:
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_calls_on_two_streams_at_once():
+    require_gpu()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cases = [scoring(3, 150_000, 8, torch.float16, k) for k in range(2)]
+    grads = [[torch.randn(1000 * i + 1, device="cuda", generator=torch.Generator(device="cuda").manual_seed(50 * k + i)) for i in range(1, 20)] for k in range(2)]
+    norms = torch.empty(2, device="cuda")
+    want = []
+    for k, (x, y, out) in enumerate(cases):
+        B.ra_token_logprobs(x, y, *out)
+        B.ra_grad_norm(grads[k], norms[k:k + 1])
+        want.append([t.clone() for t in out] + [norms[k:k + 1].clone()])
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k, (x, y, out) in enumerate(cases):
+            with torch.cuda.stream(streams[k]):
+                B.ra_token_logprobs(x, y, *out)
+                B.ra_grad_norm(grads[k], norms[k:k + 1])
+        torch.cuda.synchronize()
+        for k, (x, y, out) in enumerate(cases):
+            assert all(torch.equal(a, b) for a, b in zip(out + [norms[k:k + 1]], want[k]))
+
+
+def test_a_stream_given_by_argument():
+    require_gpu()
+    x, y, out = scoring(2, 80_000, 2, torch.float32, 3)
+    B.ra_token_logprobs(x, y, *out)
+    want = [t.clone() for t in out]
+    g = [torch.randn(100_000, device="cuda")]
+    n = torch.empty(1, device="cuda")
+    B.ra_grad_norm(g, n)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for t in out:
+        t.zero_()
+    m, to = torch.zeros(1, device="cuda"), [torch.zeros_like(g[0])]
+    spread = [torch.zeros_like(g[0])]
+    torch.cuda.synchronize()
+    B.ra_token_logprobs(x, y, *out, stream=s)
+    B.ra_grad_clip(g, 1e9, m, outs=to, stream=s)
+    B.ra_allreduce_clip(g, 1e9, m, spread, op="sum", stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert torch.equal(m, n) and torch.equal(to[0], g[0]) and torch.equal(spread[0], g[0])
+    grads = [torch.empty_like(c) for c in x]
+    B.ra_token_logprobs_backward(x, y, out[2], grads, dlogprob=out[0], stream=s)
+    s.synchronize()
+    again = [torch.empty_like(c) for c in x]
+    B.ra_token_logprobs_backward(x, y, out[2], again, dlogprob=out[0])
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_workspaces_of_the_callers():
+    """As large as they are said to be, with other memory left alone, whatever they hold."""
+    require_gpu()
+    x, y, out = scoring(2, 80_000, 2, torch.float32, 3)
+    B.ra_token_logprobs(x, y, *out)
+    want = [t.clone() for t in out]
+    g = [torch.randn(30_000 + i, device="cuda") for i in range(300)]
+    n = torch.empty(1, device="cuda")
+    B.ra_grad_norm(g, n)
+    bufs = [torch.randn(5_000_001, device="cuda") for _ in range(2)]
+    m, spread, again = torch.empty(1, device="cuda"), [torch.empty_like(bufs[0])], [torch.empty_like(bufs[0])]
+    B.ra_allreduce_clip(bufs, 1.0, m, spread)
+    for fill in (0, 255):
+        def room(size):
+            t = torch.full((size + 64,), fill, dtype=torch.uint8, device="cuda")
+            t[size:] = 77
+            return t
+        a = room(B.ra_token_logprobs_workspace(2, 80_000, 2, 20))
+        b, c = room(B.ra_grad_norm_workspace(300)), room(B.ra_allreduce_clip_workspace(5_000_001))
+        for t in out:
+            t.zero_()
+        k = torch.zeros(2, device="cuda")
+        B.ra_token_logprobs(x, y, *out, workspace=a[:-64])
+        B.ra_grad_norm(g, k[:1], workspace=b[:-64])
+        B.ra_allreduce_clip(bufs, 1.0, k[1:], again, workspace=c[:-64])
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+        assert torch.equal(k[:1], n) and torch.equal(k[1:], m) and torch.equal(spread[0], again[0])
+        for t in (a, b, c):
+            assert (t[-64:] == 77).all()
+
+
+def test_binding_refuses_what_does_not_fit():
+    require_gpu()
+    f = dict(device="cuda")
+    x = [torch.zeros((4, 5), **f), torch.zeros((4, 5), **f)]
+    y, o = torch.zeros(4, dtype=torch.int64, **f), torch.zeros(4, **f)
+    ids, tlp = torch.zeros((4, 3), dtype=torch.int64, **f), torch.zeros((4, 3), **f)
+    call = B.ra_token_logprobs
+    for bad in (dict(logprob=o.half()), dict(logprob=o[:3]), dict(entropy=torch.zeros(8, **f)[::2]), dict(lse=o.cpu()),
+                dict(top_ids=ids[:, :2], top_logprobs=tlp), dict(top_ids=ids.int()), dict(top_ids=ids[:3]), dict(top_ids=ids.flatten()),
+                dict(top_ids=ids.t().contiguous().t()), dict(top_logprobs=tlp[:, :0]), dict(top_logprobs=tlp.double())):
+        with pytest.raises((ValueError, TypeError)):
+            call(x, y, **bad)
+    for logits in (x[:1] + [x[1].half()], [x[0], x[1][:3]], [x[0][:, :4].contiguous(), x[1]], [x[0], x[1].t().contiguous().t()], [x[0].flatten(), x[1]]):
+        with pytest.raises((ValueError, TypeError)):
+            call(logits, y, lse=o)
+    with pytest.raises(TypeError):
+        call(x, y.float(), logprob=o)
+    with pytest.raises(ValueError):
+        call(x, y[:3], logprob=o[:3])
+    for bad in (dict(valid=11), dict(valid=0), dict(scale=0.0), dict(top_ids=torch.zeros((4, 11), dtype=torch.int64, **f))):
+        with pytest.raises(B.RaError):
+            call(x, y, logprob=o, **bad)
+    with pytest.raises(B.RaError):
+        call(x, None, logprob=o)                       # of which tokens?
+    with pytest.raises(B.RaError):
+        call(x, y)                                     # nothing wanted
+    back = B.ra_token_logprobs_backward
+    for grads in (x[:1], [x[0], x[1].half()], [torch.zeros((4, 6), **f), torch.zeros((4, 5), **f)]):
+        with pytest.raises((ValueError, TypeError)):
+            back(x, y, o, grads, dlogprob=o)
+    for bad in (dict(), dict(dentropy=o)):
+        with pytest.raises(B.RaError):
+            back(x, y, o, [t.clone() for t in x], **bad)
+    with pytest.raises(B.RaError):
+        back(x, None, o, [t.clone() for t in x], dlogprob=o)
+    g, n = [torch.zeros(8, **f), torch.zeros(3, **f)], torch.zeros(1, **f)
+    for bad in ([g[0], g[1].cpu()], [g[0], torch.zeros(8, **f)[::2]], [g[0], torch.zeros(3, dtype=torch.complex64, **f)]):
+        with pytest.raises((ValueError, TypeError)):
+            B.ra_grad_norm(bad, n)
+    for norm in (torch.zeros(2, **f), torch.zeros(1, dtype=torch.float64, **f), torch.zeros(1)):
+        with pytest.raises((ValueError, TypeError)):
+            B.ra_grad_norm(g, norm)
+    with pytest.raises(B.RaError):
+        B.ra_grad_norm([g[0].double()], n)
+    for outs in (g[:1], [g[1].clone(), g[0].clone()]):
+        with pytest.raises(ValueError):
+            B.ra_grad_clip(g, 1.0, n, outs=outs)
+    for bad in (dict(max_norm=0.0), dict(counted=3), dict(outs=[t.half() for t in g]), dict(outs=[g[0], g[0][:3]])):
+        with pytest.raises(B.RaError):
+            B.ra_grad_clip(g, **{"max_norm": 1.0, "norm": n, **bad})
+    with pytest.raises(B.RaError):
+        B.ra_grad_clip([g[0], g[0]], 1.0, n)           # one tensor twice, scaled twice
+    B.ra_grad_norm([g[0], g[0]], n)                    # read twice
+    bufs = [torch.zeros(8, **f), torch.zeros(8, **f)]
+    for outs in ([torch.zeros(7, **f)], [torch.zeros(8, dtype=torch.float16, **f)], []):
+        with pytest.raises((ValueError, TypeError)):
+            B.ra_allreduce_clip(bufs, 1.0, n, outs)
+    for bad in (dict(op="max"), dict(max_norm=-1.0), dict(scale=math.nan)):
+        with pytest.raises(B.RaError):
+            B.ra_allreduce_clip(bufs, **{"max_norm": 1.0, "norm": n, **bad})
+    with pytest.raises(ValueError):
+        B.ra_token_logprobs(x, y, logprob=o, workspace=torch.zeros(64, dtype=torch.uint8))
+
+
+def test_lists_that_are_marshalled_once():
+    """RankBuffers for the ranks' logits, gradients and buffers; a TensorList whose tensors change."""
+    require_gpu()
+    x, y, out = scoring(5, 1000, 2, torch.bfloat16, 8)
+    B.ra_token_logprobs(x, y, *out)
+    want = [t.clone() for t in out]
+    B.ra_token_logprobs(B.RankBuffers(x), y, *out)
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    one, two = [torch.empty_like(c) for c in x], [torch.empty_like(c) for c in x]
+    B.ra_token_logprobs_backward(x, y, out[2], one, dlogprob=out[0])
+    B.ra_token_logprobs_backward(B.RankBuffers(x), y, out[2], B.RankBuffers(two), dlogprob=out[0])
+    assert all(torch.equal(a, b) for a, b in zip(one, two))
+    bufs = [torch.randn(5000, device="cuda") for _ in range(4)]
+    a, b, n = torch.empty(5000, device="cuda"), torch.empty(5000, device="cuda"), torch.empty(2, device="cuda")
+    B.ra_allreduce_clip(bufs, 1.0, n[:1], [a])
+    B.ra_allreduce_clip(B.RankBuffers(bufs), 1.0, n[1:], B.RankBuffers([b]))
+    assert torch.equal(a, b) and n[0] == n[1]
+    g = [torch.randn(100 + i, device="cuda") for i in range(5)]
+    held = B.TensorList(g)
+    for _ in range(3):
+        for t in g:
+            t.normal_()
+        B.ra_grad_norm(held, n[:1])
+        B.ra_grad_norm(g, n[1:])
+        assert n[0] == n[1]
+
+
+def test_logits_beyond_2_to_the_32():
+    """33,000 rows of 131,072: rows, and the pieces' own offsets, pass 32 bits."""
+    require_gpu()
+    t, v = 33_000, 131_072
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = [torch.empty((t, v), device="cuda", dtype=torch.bfloat16).normal_(0, 2, generator=g)]
+    y = torch.randint(0, v, (t,), device="cuda", generator=g)
+    lp, ent, lse = (torch.empty(t, device="cuda") for _ in range(3))
+    ids = torch.empty((t, 3), device="cuda", dtype=torch.int64)
+    print("[case] 33000 x 131072", flush=True)
+    B.ra_token_logprobs(x, y, lp, ent, lse, ids)
+    at = torch.tensor([0, 1, 16_383, 16_384, 32_767, 32_768, t - 1], device="cuda")
+    want, err = A.logprobs(x[0][at], y[at], 1.0, v, 3)
+    assert torch.equal(ids[at], want[3])
+    for got, w, e, what in ((lp, want[0], err[0], "logprob"), (ent, want[1], err[1], "entropy"), (lse, want[2], err[2], "lse")):
+        R.check(got[at], w, R.rounded(w, e, torch.float32), what)
+    da = torch.randn(t, device="cuda", generator=g)
+    d, e = A.logprobs_backward(x[0][at], y[at], lse[at], None, da[at], None, 1.0, v)
+    B.ra_token_logprobs_backward(x, y, lse, x, dlogprob=da)          # in place
+    R.check(x[0][at], d, R.rounded(d, e, torch.bfloat16), "grads")
+
+
+def test_gradients_beyond_2_to_the_32():
+    require_gpu()
+    n = (1 << 32) + 12_345
+    x = torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+    x[-1] = 3.0
+    norm = torch.empty(1, device="cuda")
+    exact = math.sqrt(0.25 * (n - 1) + 9.0)
+    print("[case] a tensor of 2^32 elements", flush=True)
+    B.ra_grad_norm([x], norm)
+    assert abs(float(norm.double()) - exact) <= exact * R.U * 1.01
+    B.ra_grad_clip([x], 0.25 * exact, norm)
+    ends = torch.cat([x[:5], x[(1 << 32) - 3:(1 << 32) + 3], x[-3:]]).double()
+    want = torch.tensor([0.5] * 13 + [3.0], device="cuda", dtype=torch.float64) * 0.25
+    R.check(ends, want, R.rounded(want, want * 2.0 ** -20, torch.bfloat16), "clipped")
+    assert bool((x[:-1] == x[0]).all())
+    x.fill_(0.5)
+    x[-1] = 3.0
+    B.ra_allreduce_clip([x], 0.25 * exact, norm, op="sum")
+    assert abs(float(norm.double()) - exact) <= exact * R.U * 1.01
+    ends = torch.cat([x[:5], x[(1 << 32) - 3:(1 << 32) + 3], x[-3:]]).double()
+    R.check(ends, want, R.rounded(want, want * 2.0 ** -20, torch.bfloat16), "clipped")
+    assert bool((x[:-1] == x[0]).all())
+
+
+@pytest.mark.parametrize("t,v,valid,p,dt", [(2200, 131_072, 131_000, 8, torch.bfloat16), (1100, 131_071, 131_071, 3, torch.float32),
+                                            (30_000, 9000, 9000, 1, torch.float16)])
+def test_logits_larger_than_the_caches(t, v, valid, p, dt):
+    """More than 512 MiB: accesses past the caches where rows allow it."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(v)
+    full = torch.empty((t, v), device="cuda", dtype=dt).normal_(0, 2, generator=g)
+    full[:, valid:] = math.nan
+    full[5, :valid] = -math.inf
+    full[6, valid // 2] = math.nan
+    x = cut(full, p)
+    y = torch.randint(0, valid, (t,), device="cuda", generator=g)
+    lp, ent, lse = (torch.empty(t, device="cuda") for _ in range(3))
+    ids, tlp = torch.empty((t, 7), device="cuda", dtype=torch.int64), torch.empty((t, 7), device="cuda")
+    print(f"[case] logits larger than the caches {t} x {v}", flush=True)
+    B.ra_token_logprobs(x, y, lp, ent, lse, ids, tlp, valid=valid)
+    da, db = torch.randn(t, device="cuda", generator=g), torch.randn(t, device="cuda", generator=g)
+    grads = [torch.empty_like(c) for c in x]
+    B.ra_token_logprobs_backward(x, y, lse, grads, da, ent, db, valid=valid)
+    got = torch.cat(grads, 1)
+    for lo in range(0, t, 500):
+        k = slice(lo, min(t, lo + 500))
+        want, err = A.logprobs(full[k], y[k], 1.0, valid, 7)
+        assert torch.equal(ids[k], want[3])
+        for o, w, e, what in ((lp, want[0], err[0], "logprob"), (ent, want[1], err[1], "entropy"),
+                              (lse, want[2], err[2], "lse"), (tlp, want[4], err[4], "top_logprobs")):
+            R.check(o[k], w, R.rounded(torch.where(w.isfinite(), w, 0.0), e, torch.float32), what)
+        d, e = A.logprobs_backward(full[k], y[k], lse[k], ent[k], da[k], db[k], 1.0, valid)
+        R.check(got[k], d, R.rounded(torch.where(d.isfinite(), d, 0.0), e, dt), "grads")
