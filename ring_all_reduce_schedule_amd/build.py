@@ -77,9 +77,10 @@ def c_check_command(out=C_CHECK_BIN):
 
 C_CHECKS = os.path.join(ROOT, "tests", "c")
 HOST_CHECKS = ["host_check", "host_check_rows"]
+MORE_HOST_CHECKS = ["host_check_answers"]
 
 
-def host_check_commands(objs, out=C_CHECKS):
+def host_check_commands(objs, out=C_CHECKS, programs=None):
     """The host side of the ABI under AddressSanitizer: the library's .cpp sources again
     with the sanitizer on their host code only (each -fsanitize= right after
     -Xarch_host), linked by g++ with the kernels' objects into programs that need no GPU."""
@@ -90,7 +91,7 @@ def host_check_commands(objs, out=C_CHECKS):
     cmds = [[hipcc(), *FLAGS, "-x", "hip", "-I", INCLUDE, "-I", CSRC, "-Xarch_host", "-fsanitize=address",
              "-Xarch_host", "-fno-omit-frame-pointer", "-c", os.path.join(CSRC, h + ".cpp"), "-o", o]
             for h, o in zip(host, checked)]
-    for name in HOST_CHECKS:
+    for name in HOST_CHECKS if programs is None else programs:
         main = os.path.join(BUILD, name + ".o")
         cmds += [
             ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address", "-fno-omit-frame-pointer",
@@ -120,7 +121,7 @@ def build(verbose=False):
         sys.stderr.write("\n".join(noise) + "\n")
     os.replace(tmp, LIB)
     noise += _run(c_check_command())
-    for cmd in host_check_commands(objs):
+    for cmd in host_check_commands(objs, programs=HOST_CHECKS + MORE_HOST_CHECKS):
         noise += _run(cmd)
     if verbose and noise:
         sys.stderr.write("\n".join(noise) + "\n")
