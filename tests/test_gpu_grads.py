@@ -119,6 +119,18 @@ def test_gradients_of_any_size(dt, size):
     R.check(out, w, tol, "clipped")
 
 
+def test_a_norm_beyond_float32():
+    """It is infinite in float32; the factor, which comes from it in float64, is not zero."""
+    require_gpu()
+    x = torch.full((1000,), 2e38, device="cuda")
+    norm, out = torch.empty(1, device="cuda"), torch.empty(1000, device="cuda")
+    n = 2e38 * math.sqrt(1000)
+    B.ra_grad_clip([x], 10.0, norm, outs=[out])
+    assert norm.item() == math.inf
+    w, tol = A.scaled(x, 10.0 / n, 10.0 / n * 2.0 ** -20, torch.float32)
+    R.check(out, w, tol, "clipped")
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 def test_a_norm_that_is_not_finite(bad):
     require_gpu()

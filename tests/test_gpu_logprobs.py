@@ -154,6 +154,56 @@ def test_logits_of_any_size(size, v, t):
         R.check(got, w, R.rounded(w, e, torch.float32), what)
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 30.0, 1e5, 1e12])
+@pytest.mark.parametrize("t,v", [(3, 60_000), (150, 5000)])
+def test_temperatures_of_any_size(scale, t, v):
+    require_gpu()
+    x, y, _ = make(t, v, torch.bfloat16, t, v)
+    lp, ent, lse = (torch.empty(t, device="cuda") for _ in range(3))
+    ids, tlp = torch.empty((t, 9), dtype=torch.int64, device="cuda"), torch.empty((t, 9), device="cuda")
+    B.ra_token_logprobs(cut(x, 4), y, lp, ent, lse, ids, tlp, scale=scale)
+    want, err = A.logprobs(x, y, scale, v, 9)
+    assert torch.equal(ids, want[3])
+    for got, w, e, what in ((lp, want[0], err[0], "logprob"), (ent, want[1], err[1], "entropy"),
+                            (lse, want[2], err[2], "lse"), (tlp, want[4], err[4], "top_logprobs")):
+        R.check(got, w, R.rounded(torch.where(w.isfinite(), w, 0.0), e, torch.float32), what)
+
+
+def test_tokens_far_outside_the_vocabulary():
+    require_gpu()
+    x = torch.randn((6, 100), device="cuda")
+    y = torch.tensor([2 ** 40, -2 ** 40, 2 ** 32 + 5, 99, 100, -1], device="cuda")
+    lp, lse = torch.empty(6, device="cuda"), torch.empty(6, device="cuda")
+    B.ra_token_logprobs(cut(x, 3), y, lp, lse=lse)
+    want, err = A.logprobs(x, y, 1.0, 100, 1)
+    R.check(lp, want[0], R.rounded(torch.where(want[0].isfinite(), want[0], 0.0), err[0], torch.float32), "logprob")
+    grads, da = [torch.empty_like(c) for c in cut(x, 3)], torch.ones(6, device="cuda")
+    B.ra_token_logprobs_backward(cut(x, 3), y, lse, grads, da)
+    d, e = A.logprobs_backward(x, y, lse, None, da, None, 1.0, 100)
+    R.check(torch.cat(grads, 1), d, R.rounded(torch.where(d.isfinite(), d, 0.0), e, torch.float32), "grads")
+
+
+def test_more_rows_than_one_launch_takes():
+    """Rows of eight columns, a workgroup each: a launch has fewer than 2^32 threads."""
+    require_gpu()
+    t, v = (1 << 25) + 77, 8
+    x = torch.empty((t, v), device="cuda", dtype=torch.bfloat16).normal_()
+    y = torch.randint(0, v, (t,), device="cuda")
+    lp, lse, ids = torch.empty(t, device="cuda"), torch.empty(t, device="cuda"), torch.empty((t, 2), device="cuda", dtype=torch.int32)
+    print(f"[case] {t} rows", flush=True)
+    B.ra_token_logprobs([x], y.int(), lp, lse=lse, top_ids=ids)
+    da = torch.randn(t, device="cuda")
+    grads = torch.empty_like(x)
+    B.ra_token_logprobs_backward([x], y, lse, [grads], da)
+    for lo in (0, 1 << 24, (1 << 25) - 1000, t - 1000):
+        k = slice(lo, lo + 1000)
+        want, err = A.logprobs(x[k], y[k], 1.0, v, 2)
+        assert torch.equal(ids[k].long(), want[3])
+        R.check(lp[k], want[0], R.rounded(want[0], err[0], torch.float32), "logprob")
+        d, e = A.logprobs_backward(x[k], y[k], lse[k], None, da[k], None, 1.0, v)
+        R.check(grads[k], d, R.rounded(d, e, torch.bfloat16), "grads")
+
+
 BACKWARD = [c for c in CASES if c[0:3] not in ((63, 3, 1 << 24),)]
 
 
