@@ -351,15 +351,18 @@ __device__ __forceinline__ Picked pick_row(const LogpArgs& a, int64_t row, Range
   }, [&](uint32_t key, auto f) { each_in<DT, MODE>(a, row, g, top, key, f); });
 }
 
-// f(rank, place) for the first k of some places.
+// f(rank, place) for the first k of some places, four threads to each.
 template <int G, typename F>
 __device__ __forceinline__ void in_order(const Picked& t, int k, F f) {
-  for (int i = threadIdx.x; i < t.n; i += G) {
+  const int sub = threadIdx.x % 4;
+  for (int i = threadIdx.x / 4; i < t.n; i += G / 4) {
     const uint64_t x = t.list[i];
-    int rank = 0;
+    uint32_t rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < t.n; ++j) rank += t.list[j] > x;
-    if (rank < k) f(rank, x);
+    for (int j = sub; j < t.n; j += 4) rank += t.list[j] > x;
+    rank += dpp<kDppNeighbour>(rank);
+    rank += dpp<kDppPair>(rank);
+    if (sub == 0 && rank < (uint32_t)k) f((int)rank, x);
   }
 }
 

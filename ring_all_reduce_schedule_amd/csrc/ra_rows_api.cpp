@@ -70,17 +70,25 @@ struct Span {
   bool write;
 };
 
-// Whether no byte is written by one array and in another.  Sorts the list, unless it is.
-int check_spans(Span* list, int64_t n) {
-  auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+bool before(const Span& a, const Span& b) { return a.lo < b.lo; }
+// Lists mostly come in the order of their addresses, for which a look will do.
+void sort_spans(Span* list, int64_t n) {
   if (!std::is_sorted(list, list + n, before)) std::sort(list, list + n, before);
+}
+
+int overlap(const Span& a, const Span& b) {
+  return fail(RA_ERR_ALIAS, "%s (%d) and %s (%d) overlap", a.what, a.index, b.what, b.index);
+}
+
+// Whether no byte is written by one array and in another, of a sorted list.
+int check_spans(const Span* list, int64_t n) {
   const Span *read = nullptr, *written = nullptr;   // the ones so far that end last
   for (int64_t i = 0; i < n; ++i) {
     const Span& x = list[i];
     const Span* with = written && x.lo < written->hi         ? written
                        : x.write && read && x.lo < read->hi ? read
                                                              : nullptr;
-    if (with) return fail(RA_ERR_ALIAS, "%s (%d) and %s (%d) overlap", with->what, with->index, x.what, x.index);
+    if (with) return overlap(*with, x);
     const Span*& last = x.write ? written : read;
     if (!last || x.hi > last->hi) last = &x;
   }
@@ -122,7 +130,10 @@ class Arrays {
     }
     return add(what, index, ptr, bytes, elem, true);
   }
-  int overlaps() { return check_spans(list_, n_); }
+  int overlaps() {
+    sort_spans(list_, n_);
+    return check_spans(list_, n_);
+  }
   bool al() const { return aligned_; }
 
  private:
@@ -281,40 +292,48 @@ int check_list(ra::TensorListArgs& a, float* norm, void* workspace, int64_t have
   const int64_t need = ra::grad_norm_bytes(a.n);
   if (have < need)
     return fail(RA_ERR_INVALID_ARG, "workspace of %lld bytes, need %lld", (long long)have, (long long)need);
-  // host memory, for the call alone
-  std::unique_ptr<Span[]> list(new (std::nothrow) Span[2 * a.n + 2]);
-  if (!list) return fail(RA_ERR_UNSUPPORTED, "no host memory for %lld tensors", (long long)a.n);
-  int64_t m = 0, elements = 0, bytes = 0;
-  auto add = [&](const char* what, int64_t i, const void* ptr, int64_t bytes, int elem, bool write) {
+  // host memory, for the call alone: the tensors, the outputs, and the two lists in one
+  std::unique_ptr<Span[]> room(new (std::nothrow) Span[4 * a.n + 1]);
+  if (!room) return fail(RA_ERR_UNSUPPORTED, "no host memory for %lld tensors", (long long)a.n);
+  Span *read = room.get(), *written = read + a.n, *all = written + a.n;
+  int64_t reads = 0, writes = 0, elements = 0, bytes = 0;
+  auto make = [](Span* to, const char* what, int64_t i, const void* ptr, int64_t bytes, int elem, bool write) {
     if (!ptr) return fail(RA_ERR_INVALID_ARG, "%s[%lld] is NULL", what, (long long)i);
     const uintptr_t at = reinterpret_cast<uintptr_t>(ptr);
     if (at % elem != 0)
       return fail(RA_ERR_MISALIGNED, "%s[%lld] = %p is not on a boundary of its %d-byte elements", what, (long long)i,
                   ptr, elem);
-    list[m++] = {at, at + (uint64_t)bytes, what, (int)i, write};
+    *to = {at, at + (uint64_t)bytes, what, (int)i, write};
     return (int)RA_OK;
   };
-  for (int64_t i = 0; i < a.n; ++i) {
+  Span own[2];      // these overlap nothing
+  rc = make(&own[0], "norm", 0, norm, 4, 4, true);
+  if (rc == RA_OK) rc = make(&own[1], "workspace", 0, workspace, need, 16, true);
+  if (rc == RA_OK && own[0].lo < own[1].hi && own[1].lo < own[0].hi) rc = overlap(own[0], own[1]);
+  for (int64_t i = 0; i < a.n && rc == RA_OK; ++i) {
     const int64_t count = a.counts[i];
     if (count < 0) return fail(RA_ERR_INVALID_ARG, "counts[%lld] = %lld", (long long)i, (long long)count);
     if (count > kListElements || (elements += count) > kListElements)
       return fail(RA_ERR_UNSUPPORTED, "more than 2^40 elements in a call");
     rc = check_real("dtype", a.types[i]);
     if (rc == RA_OK && a.out && a.out_types) rc = check_second("out_dtype", a.out_types[i], a.types[i]);
-    if (rc != RA_OK) return rc;
-    if (count == 0) continue;
+    if (rc != RA_OK || count == 0) continue;
     const int e = ra::elem_bytes(a.types[i]);
     const int to = a.out && a.out_types ? a.out_types[i] : a.types[i], eo = ra::elem_bytes(to);
     const bool same = a.out && a.out[i] == a.in[i] && to == a.types[i];
-    rc = add("tensors", i, a.in[i], count * e, e, same);
-    if (rc == RA_OK && a.out && !same) rc = add("outs", i, a.out[i], count * eo, eo, true);
-    if (rc != RA_OK) return rc;
+    rc = make(&read[reads++], "tensors", i, a.in[i], count * e, e, same);
+    if (rc == RA_OK && a.out && !same) rc = make(&written[writes++], "outs", i, a.out[i], count * eo, eo, true);
     bytes += count * (e + (a.out ? eo : 0));
   }
+  if (rc != RA_OK) return rc;
   a.stream = bytes > ra::kStreamingBytes;
-  rc = add("norm", 0, norm, 4, 4, true);
-  if (rc == RA_OK) rc = add("workspace", 0, workspace, need, 16, true);
-  return rc == RA_OK ? check_spans(list.get(), m) : rc;
+  sort_spans(read, reads);
+  sort_spans(written, writes);
+  std::merge(read, read + reads, written, written + writes, all, before);
+  for (int64_t i = 0; i < reads + writes; ++i)
+    for (const Span& x : own)
+      if (all[i].lo < x.hi && x.lo < all[i].hi) return overlap(all[i], x);
+  return check_spans(all, reads + writes);
 }
 
 }  // namespace
