@@ -528,9 +528,11 @@ __global__ __launch_bounds__(TOP ? kJoinThreads : 64) void k_logp_join(LogpArgs 
   }
 }
 
-// The gradient: `splits` workgroups to a row, each wave with M chunks: two beyond the caches, one within
-// them (us with one, two, three and four; 4096 x 131072 bfloat16: 451, 346, 375, 362; 517 x 50017 float32:
-// 37.0, 39.1, 36.4, 38.0; one row of 32000: 3.6, 4.0, -, 4.9).
+// The gradient: `splits` workgroups to a row, each wave with M chunks: four where that leaves the GPU
+// eight workgroups to a compute unit, one where not (us with one, two and four; 64 rows of 32000 bfloat16:
+// 5.2, 5.5, 6.5; 256 of 128000: 28.6, 28.2, 25.3; 4096 of 32000: 145, 123, 111).  Beyond the caches, two where
+// all chunks are whole ones (4096 x 131072: 451, 348, 367; 4096 x 110592: -, 309, 322), four where pieces leave
+// a rest (4096 x 128000: -, 418, 357).
 constexpr int kGradThreads = 256, kGradWaves = kGradThreads / 64;
 
 // A token's weights and what its gradient is made with.
@@ -649,11 +651,25 @@ hipError_t grad_go(const LogpArgs& args, hipStream_t s) {
   return hipSuccess;
 }
 
+// Past the caches where they do not hold the call (4096 x 128000 bfloat16: 354 us against 392), but not
+// float32, of which a lane's accesses are half lines (2048 x 131072: 412 against 388).
 template <int DT>
-hipError_t bwd_go(const LogpArgs& a, bool al, bool big, hipStream_t s) {
+hipError_t stream_go(const LogpArgs& a, hipStream_t s) {
+  return a.total == a.whole * a.p ? grad_go<DT, kStream, 2>(a, s) : grad_go<DT, kStream, 4>(a, s);
+}
+template <int DT, int M>
+hipError_t bwd_go(const LogpArgs& a, bool al, hipStream_t s) {
+  return al ? grad_go<DT, kAligned, M>(a, s) : grad_go<DT, kOdd, M>(a, s);
+}
+
+constexpr int64_t kGradFew = 2048 * kGradWaves * 4;      // chunks
+
+template <int DT>
+hipError_t bwd_size(const LogpArgs& a, bool al, bool big, hipStream_t s) {
   if (a.cut.base < kU) return grad_go<DT, kTiny, 1>(a, s);
-  if (big) return al ? grad_go<DT, kStream, 2>(a, s) : grad_go<DT, kOdd, 2>(a, s);
-  return al ? grad_go<DT, kAligned, 1>(a, s) : grad_go<DT, kOdd, 1>(a, s);
+  if constexpr (DT != 1)
+    if (al && big) return stream_go<DT>(a, s);
+  return a.tokens * a.total < kGradFew ? bwd_go<DT, 1>(a, al, s) : bwd_go<DT, 4>(a, al, s);
 }
 
 }  // namespace
@@ -680,9 +696,9 @@ hipError_t launch_logp(const LogpArgs& a, int dtype, int access, hipStream_t s) 
 }
 
 hipError_t launch_logp_bwd(const LogpArgs& a, int dtype, bool al, bool big, hipStream_t s) {
-  if (dtype == 1) return bwd_go<1>(a, al, big, s);
-  if (dtype == 2) return bwd_go<2>(a, al, big, s);
-  return bwd_go<3>(a, al, big, s);
+  if (dtype == 1) return bwd_size<1>(a, al, big, s);
+  if (dtype == 2) return bwd_size<2>(a, al, big, s);
+  return bwd_size<3>(a, al, big, s);
 }
 
 }  // namespace ra
