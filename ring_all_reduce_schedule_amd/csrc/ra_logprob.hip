@@ -626,7 +626,12 @@ hipError_t rows_go(const LogpArgs& args, hipStream_t s) {
 template <int DT, int MODE>
 hipError_t logp_size(const LogpArgs& a, hipStream_t s) {
   if (a.splits > 1) return rows_go<DT, 256, MODE>(a, s);
-  return a.total <= 8 ? rows_go<DT, 128, MODE>(a, s) : rows_go<DT, 512, MODE>(a, s);
+  // threads to a row: fewer for short rows, of which a compute unit then holds more, and the others' loads
+  // cover a row's end; as many as pay off where rows are too few for that (top 20, us with 512, 256 and 128;
+  // 4096 x 32000: 66, 59, 70; 16384 x 8192: 147, 83, 73; 300 x 32000: 14.3, 15.4, 22.7)
+  const bool many = a.tokens >= 2048;
+  if (a.total <= (many ? 16 : 8)) return rows_go<DT, 128, MODE>(a, s);
+  return many && a.total <= 128 ? rows_go<DT, 256, MODE>(a, s) : rows_go<DT, 512, MODE>(a, s);
 }
 
 template <int DT>
