@@ -13,6 +13,17 @@
 //
 // The sums have a fixed order: a workgroup's elements, its threads, and the
 // workgroups, whose number depends on the sizes alone.
+//
+// All of it is bound by memory, and each pass moves 1.00 times the bytes that it has to
+// (HBM counters).  What decides the rate is how the accesses go past the caches, how much a thread
+// has under way, and whether streams are read and written in turns.  Measured on MI355X, where a copy of
+// 8 GiB runs at 6.55 TB/s and reads alone at 7.0:
+//   norm of 1.2 10^9 bfloat16 gradients, 219 tensors    345 us, 6.9 TB/s
+//   the same clipped into other buffers                 1128 us: the norm, and 775 us at 6.1 TB/s
+//   8 x 256 MiB float32 averaged, clipped, to all 8     784 us: 393 us for 2.4 GB, 9 streams at equal offsets,
+//                                                       332 us for 2.4 GB of which the caches have some
+//   9 x 1,000,003 bfloat16 summed, clipped, to all 9    14.2 us: 5.5 and 7.0 in two launches
+//   norm of 75 tensors, 24 MB in the caches             5.4 us and 2.4 for the sum of the parts
 #include "ra_rows.h"
 
 namespace ra {

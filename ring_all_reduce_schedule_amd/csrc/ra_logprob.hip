@@ -13,11 +13,24 @@
 // value, NaN, +inf, logits beyond 10^7) is done again with m subtracted first.
 //
 // The k best columns by (logit descending, column ascending): in the same pass each thread
-// keeps the largest logit of every 32 that it reads.  The k-th largest of the threads' own
-// maxima bounds the k-th best logit from below, and only the groups whose maximum reaches
-// that bound are read again, some k of a row's thousands.  Their elements at or above the
-// bound are put in order by counting, for each, the ones in front of it.  Where too many
-// reach the bound (ties), it is raised first, by halving the interval of (logit, column).
+// keeps the largest logit of every 32 that it reads.  The k-th largest of the maxima of 128
+// sets of threads bounds the k-th best logit from below, and only the groups whose maximum reaches
+// that bound are read again, some k of a row's thousands, a thread to each unit of eight columns.
+// The elements at or above the bound are put in order by counting, for each, the ones in front of it.
+// Where too many reach the bound (ties), it is raised first, by halving the interval of (logit, column).
+// Few rows are cut into parts, a workgroup each, whose sums and best columns a second launch joins.
+//
+// Large calls are bound by memory: without the exponentials and the sums, 4096 x 131072 take 181 us where they
+// take 188 with them.  Measured on MI355X (GPU time; a copy of 8 GiB runs at 6.55 TB/s, reads alone at 7.0):
+//   4096 x 131072 bfloat16, 8 ranks     182 us, 5.9 TB/s; top 20 184, top 64 207
+//   16384 x 131072                      643 us, 6.7 TB/s: a call's last rows leave the GPU unevenly
+//   1003 x 50017 float32, 9 ranks       35 us, 5.7 TB/s; top 64 44
+//   16 x 128000 bfloat16, top 20        12.5 us in two launches
+//   1 x 32000 float16, top 5            9.5 us in one
+//   gradient of 4096 x 131072           348 us, 6.2 TB/s
+// It reads 1.05 times the logits' bytes with 20 alternatives of 131072 bfloat16 columns, 1.28 times with 64
+// of 50017 float32 ones (HBM counters): the groups that are read again, a line for each unit.  The gradient reads
+// and writes 1.00 times what it has to.
 #include "ra_vocab.h"
 
 namespace ra {
@@ -528,11 +541,12 @@ __global__ __launch_bounds__(TOP ? kJoinThreads : 64) void k_logp_join(LogpArgs 
   }
 }
 
-// The gradient: `splits` workgroups to a row, each wave with M chunks: four where that leaves the GPU
-// eight workgroups to a compute unit, one where not (us with one, two and four; 64 rows of 32000 bfloat16:
-// 5.2, 5.5, 6.5; 256 of 128000: 28.6, 28.2, 25.3; 4096 of 32000: 145, 123, 111).  Beyond the caches, two where
-// all chunks are whole ones (4096 x 131072: 451, 348, 367; 4096 x 110592: -, 309, 322), four where pieces leave
-// a rest (4096 x 128000: -, 418, 357).
+// The gradient: `splits` workgroups to a row, each wave with M chunks.  16-bit types: four where that leaves
+// the GPU eight workgroups to a compute unit, one where not (us with one, two and four; 64 rows of 32000
+// bfloat16: 5.2, 5.5, 6.5; 256 of 128000: 28.6, 28.2, 25.3; 4096 of 32000: 145, 123, 111).  Beyond the caches, two
+// where all chunks are whole ones (4096 x 131072: 451, 348, 367; 4096 x 110592: -, 309, 322), four where pieces
+// leave a rest (4096 x 128000: -, 418, 357).  float32, whose chunks are twice as large: one, beyond the caches two
+// (517 x 50017: 45.5, 48, 49.2; 2048 x 131072: 424, 412, 423).
 constexpr int kGradThreads = 256, kGradWaves = kGradThreads / 64;
 
 // A token's weights and what its gradient is made with.
@@ -656,25 +670,24 @@ hipError_t grad_go(const LogpArgs& args, hipStream_t s) {
   return hipSuccess;
 }
 
-// Past the caches where they do not hold the call (4096 x 128000 bfloat16: 354 us against 392), but not
-// float32, of which a lane's accesses are half lines (2048 x 131072: 412 against 388).
-template <int DT>
-hipError_t stream_go(const LogpArgs& a, hipStream_t s) {
-  return a.total == a.whole * a.p ? grad_go<DT, kStream, 2>(a, s) : grad_go<DT, kStream, 4>(a, s);
-}
 template <int DT, int M>
-hipError_t bwd_go(const LogpArgs& a, bool al, hipStream_t s) {
+hipError_t grad_rows(const LogpArgs& a, bool al, hipStream_t s) {
   return al ? grad_go<DT, kAligned, M>(a, s) : grad_go<DT, kOdd, M>(a, s);
 }
 
 constexpr int64_t kGradFew = 2048 * kGradWaves * 4;      // chunks
 
+// Past the caches where they do not hold the call (4096 x 128000 bfloat16: 354 us against 392), but not
+// float32, of which a lane's accesses are half lines (2048 x 131072: 412 against 388).
 template <int DT>
-hipError_t bwd_size(const LogpArgs& a, bool al, bool big, hipStream_t s) {
+hipError_t bwd_go(const LogpArgs& a, bool al, bool big, hipStream_t s) {
   if (a.cut.base < kU) return grad_go<DT, kTiny, 1>(a, s);
-  if constexpr (DT != 1)
-    if (al && big) return stream_go<DT>(a, s);
-  return a.tokens * a.total < kGradFew ? bwd_go<DT, 1>(a, al, s) : bwd_go<DT, 4>(a, al, s);
+  if constexpr (DT == 1) {
+    return big ? grad_rows<DT, 2>(a, al, s) : grad_rows<DT, 1>(a, al, s);
+  } else {
+    if (al && big) return a.total == a.whole * a.p ? grad_go<DT, kStream, 2>(a, s) : grad_go<DT, kStream, 4>(a, s);
+    return a.tokens * a.total < kGradFew ? grad_rows<DT, 1>(a, al, s) : grad_rows<DT, 4>(a, al, s);
+  }
 }
 
 }  // namespace
@@ -701,9 +714,9 @@ hipError_t launch_logp(const LogpArgs& a, int dtype, int access, hipStream_t s) 
 }
 
 hipError_t launch_logp_bwd(const LogpArgs& a, int dtype, bool al, bool big, hipStream_t s) {
-  if (dtype == 1) return bwd_size<1>(a, al, big, s);
-  if (dtype == 2) return bwd_size<2>(a, al, big, s);
-  return bwd_size<3>(a, al, big, s);
+  if (dtype == 1) return bwd_go<1>(a, al, big, s);
+  if (dtype == 2) return bwd_go<2>(a, al, big, s);
+  return bwd_go<3>(a, al, big, s);
 }
 
 }  // namespace ra

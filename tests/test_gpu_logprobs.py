@@ -73,6 +73,7 @@ CASES = [
     (4, 140, 33000, 33000, 1, "f32", 0), (8, 140, 65536, 65536, 64, "bf16", 0), (3, 113, 70001, 70000, 20, "bf16", 1),
     (8, 134, 131072, 131072, 20, "bf16", 0), (1, 150, 151_937, 151_900, 64, "f16", 0), (2, 150, 140_000, 140_000, 20, "f32", 0),
     (8, 300, 295_000, 295_000, 20, "bf16", 0), (5, 330, 300_007, 300_000, 64, "f16", 0), (3, 13, 1_000_003, 1_000_000, 64, "bf16", 0),
+    (1, 2050, 8192, 8190, 20, "bf16", 0), (3, 2049, 50_003, 50_003, 64, "f32", 0), (8, 2300, 32_000, 32_000, 20, "f16", 0),
     (63, 3, 1 << 24, 1 << 24, 64, "bf16", 0), (2, 12, 1 << 20, 1 << 20, 20, "f32", 0),
 ]
 
