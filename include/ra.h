@@ -540,7 +540,8 @@ int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_
  *   workspace  ra_token_logprobs_workspace bytes
  * Logits of -inf are masked columns: they come last.  A row all of whose columns are -inf
  * has lse = -inf, entropy 0 and log probabilities of -inf.  A logit of +inf or NaN makes
- * its row's numbers NaN; NaN counts as the largest logit.
+ * its row's numbers NaN; NaN counts as the largest logit.  An lse beyond float32 (scaled
+ * logits of 10^38) is infinite; the log probabilities and the entropy come without it.
  */
 int ra_token_logprobs(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid, int dtype,
                       float scale, const void* ids, int id_dtype, float* logprob, float* entropy,
@@ -556,7 +557,7 @@ int ra_token_logprobs_workspace(int64_t tokens, int64_t vocab, int p, int top, i
  *            most.  dlogprob needs ids; that of a token whose id is below 0 is taken as 0.
  *   grads    p arrays like logits; grads[r] may be logits[r]
  * A token whose two gradients are 0 gets zeros whatever its logits hold, and so does one
- * all of whose columns are -inf.  An id from `valid` on, or an lse of +inf or NaN, makes
+ * whose lse is -inf (all of its columns are).  An id from `valid` on, or an lse of +inf or NaN, makes
  * the token's gradient NaN.  Columns from `valid` on get zeros.
  */
 int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid,
@@ -631,8 +632,9 @@ int ra_grad_norm_workspace(int64_t n, int64_t* bytes);
  *   norm      the norm before clipping, scale included
  *   workspace  ra_grad_norm_workspace bytes
  * c is computed in float64 and rounded to float32.  The products are float32, rounded
- * once.  With a norm that is not finite c is 0 or NaN: look at norm before the outputs
- * are used.  Tensors that are scaled in place with c = 1 are not written.
+ * once.  Gradients that are not finite make norm infinite or NaN, and c 0 or NaN: look at
+ * norm before the outputs are used.  (Finite ones whose norm is beyond float32 make norm
+ * infinite, too; c, from the norm in float64, still clips them.)  Tensors that are scaled in place with c = 1 are not written.
  */
 int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes, int64_t n,
                  int64_t counted, float max_norm, float scale, void* const* outs, const int* out_dtypes,

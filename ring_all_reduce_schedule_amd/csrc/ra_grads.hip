@@ -93,11 +93,11 @@ __global__ __launch_bounds__(1024) void k_finish(ClipRule r, float* to) {
 
 // A lane moves N consecutive elements of each array at a time, at most 16 bytes, so that a wave's
 // accesses are whole lines: 8 elements, or 4 where one of the arrays is float32.  (A lane that
-// moved 8 float32, as two accesses 16 bytes apart, wrote half lines: 889 us where it is 497 now,
-// 8 x 256 MiB.)  Arrays start on any boundary of their elements, for which gfx950 issues the same
-// accesses.  Where a run of elements ends inside a lane's, those are moved back to end there, and
-// the first `lo` of them, which are another lane's, are loaded and not used.  Runs shorter than N
-// go a lane to an element.
+// moved 8 float32, as two accesses 16 bytes apart, wrote half lines: the pass that writes 8 x 256 MiB
+// took 889 us, and 497 with 16 bytes a lane, before what makes it 332 now.)  Arrays start on any
+// boundary of their elements, for which gfx950 issues the same accesses.  Where a run of elements ends
+// inside a lane's, those are moved back to end there, and the first `lo` of them, which are another
+// lane's, are loaded and not used.  Runs shorter than N go a lane to an element.
 template <int N> struct Some {
   float x[N];
 };
@@ -230,7 +230,7 @@ template <int N, bool OUT> constexpr int tensors(const Batch<N, OUT>&) { return 
 // Accesses of a thread to a tile.  What the norm reads: 32 elements, all under way together.  The pass
 // that scales beyond the caches has one access: read and written streams go best that way (2.4 GB into
 // 2.4 GB: 742 us, two accesses 820, four 833), in workgroups that take a tile each (884 in ones that stay).
-// Where the caches serve it, four, in workgroups that stay (33 MB into 66 MB: 22 us, one access 27).
+// Where the caches serve it, four, in workgroups that stay (44 MB into 88 MB: 24.6 us, one access 27).
 template <bool NT> constexpr int kScaleLoads = NT ? 1 : 4;
 constexpr int kReadTile = kThreads * 32;
 template <bool OUT>
@@ -253,7 +253,7 @@ __device__ __forceinline__ int tensor_of(const Batch<N, OUT>& b, uint32_t t) {
 }
 
 // The same by halving: eight scalar loads, one behind the other, from the scalar cache.  For launches
-// of many workgroups that look up one tile each (2.4 GB into 2.4 GB: 800 us).
+// of many workgroups that look up one tile each (2.4 GB into 2.4 GB: 775 us).
 template <int N, bool OUT>
 __device__ __forceinline__ int tensor_by_halving(const Batch<N, OUT>& b, uint32_t t) {
   int lo = 0;

@@ -341,6 +341,34 @@ def test_lists_that_are_marshalled_once():
         assert n[0] == n[1]
 
 
+def test_gradients_in_rank_buffers():
+    """The norm of and clipping by a RankBuffers, and into one."""
+    require_gpu()
+    g = [torch.randn(777, device="cuda") for _ in range(3)]
+    n = torch.empty(2, device="cuda")
+    B.ra_grad_norm(g, n[:1])
+    B.ra_grad_norm(B.RankBuffers(g), n[1:])
+    assert n[0] == n[1]
+    one, two = ([torch.empty_like(t) for t in g] for _ in range(2))
+    B.ra_grad_clip(g, 1.0, n[:1], one)
+    B.ra_grad_clip(B.RankBuffers(g), 1.0, n[1:], B.RankBuffers(two))
+    assert all(torch.equal(a, b) for a, b in zip(one, two)) and n[0] == n[1]
+
+
+def test_tensor_list_out_of_date():
+    require_gpu()
+    g, n = [torch.randn(64, device="cuda") for _ in range(2)], torch.empty(1, device="cuda")
+    held = B.TensorList(g)
+    room = torch.zeros(4096, device="cuda")
+    g[0].set_(room[1024:1088])
+    with pytest.raises(ValueError, match="re-pointed"):
+        B.ra_grad_norm(held, n)
+    with pytest.raises(ValueError, match="re-pointed"):
+        B.ra_grad_clip([room[:64], room[64:128]], 1.0, n, held)
+    B.ra_grad_norm(B.TensorList([]), n)
+    assert n[0] == 0
+
+
 def test_logits_beyond_2_to_the_32():
     """33,000 rows of 131,072: rows, and the pieces' own offsets, pass 32 bits."""
     require_gpu()
