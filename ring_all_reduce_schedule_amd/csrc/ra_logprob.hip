@@ -84,17 +84,12 @@ __device__ __forceinline__ Stat row_join(Stat t) {
 __device__ __forceinline__ Stat lane_stat(const Stat& t, int lane) {
   return {lane_value(t.m, lane), lane_value(t.c, lane), lane_value(t.z, lane), lane_value(t.w, lane)};
 }
-__device__ __forceinline__ Stat join2(const Stat& a, const Stat& b) {
-  const float c = __builtin_fmaxf(a.c, b.c), da = a.c - c, db = b.c - c, ra = exp2_of(da), rb = exp2_of(db);
-  return {__builtin_fmaxf(a.m, b.m), c, a.z * ra + b.z * rb,
-          ra * __builtin_fmaf(da, a.z, a.w) + rb * __builtin_fmaf(db, b.z, b.w)};
-}
 
-// Over the workgroup of at most 16 waves; every lane gets it.  `lds` is free again at the next
-// barrier.
+// Over the workgroup of at most 16 waves, in each of which m and c are the same; every lane gets it.
+// `lds` is free again at the next barrier.
 __device__ __forceinline__ Stat block_join(Stat t, Stat* lds, int waves) {
-  t = row_join(t);
-  t = join2(join2(lane_stat(t, 0), lane_stat(t, 16)), join2(lane_stat(t, 32), lane_stat(t, 48)));
+  t.z = wave_sum(t.z);
+  t.w = wave_sum(t.w);
   const int lane = threadIdx.x % 64;
   if (lane == 0) lds[threadIdx.x / 64] = t;
   __syncthreads();
@@ -178,6 +173,7 @@ __device__ __forceinline__ int slack(int k) { return 4 + k / 4; }
 
 template <int G> struct Pick {
   uint64_t best[kCap];
+  const void* x[kMaxRanks];      // the pieces, for threads that read different ones
   uint32_t lanes[G];
   union {
     uint16_t work[kWork];
@@ -222,6 +218,35 @@ __device__ __forceinline__ void keep(Pick<G>* P, uint64_t x) {
   if (i < kCap) P->best[i] = x;
 }
 
+// Element i of a unit, where i is known at run time only.
+template <int DT>
+__device__ __forceinline__ float unit_at(const Unit<DT>& u, int i) {
+  float x = unit_get<DT>(u, 0);
+#pragma unroll
+  for (int j = 1; j < kU; ++j) x = i == j ? unit_get<DT>(u, j) : x;
+  return x;
+}
+
+// Keeps the elements of a unit whose order reaches the bound.
+template <int DT, int G>
+__device__ __forceinline__ void keep_unit(const LogpArgs& a, const Chunk& s, const Lane& l, const Unit<DT>& u,
+                                          uint32_t bound, Pick<G>* P) {
+  const float least = logit_of(bound);
+  const bool nan = bound == 0xffffffffu;      // only NaN reaches it
+  uint32_t hits = 0;
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    const float x = unit_get<DT>(u, i);
+    const bool hit = !(x < least) && !(nan && x == x) && counts(s, l, a.valid, i);
+    hits |= hit ? 1u << i : 0u;
+  }
+  if (hits == 0) return;
+  for (int at = atomicAdd(&P->n, __builtin_popcount(hits)); hits != 0; hits &= hits - 1, ++at) {
+    const int i = __builtin_ctz(hits);
+    if (at < kCap) P->best[at] = place_of(order_of(unit_at<DT>(u, i)), s.col0 - s.c0 + l.c + i);
+  }
+}
+
 // The k-th largest of the maxima of kSets sets of threads, or a smaller one that at most slack(k) more sets
 // reach; by one wave.  (With a set for each thread, more of the k best are sets' maxima, and the
 // bound is higher; 128 sets bring 22 of the row's elements for 20, 89 for 64, in a quarter of the
@@ -239,14 +264,15 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t* v, int k) {
   uint32_t hi = wave_max_u32(max(x, y)), lo = ~wave_max_u32(~min(x, y));
   if (reach(hi) >= k) return hi;
   while (hi - lo > 1) {            // lo is reached by k at least, hi by fewer
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int n = reach(mid);
-    if (n < k) {
-      hi = mid;
-    } else {
-      lo = mid;
-      if (n <= k + slack(k)) break;
-    }
+    // three at once take as long as one
+    const uint32_t d = (hi - lo) / 4 + (hi - lo < 4), m1 = lo + d, m2 = min(m1 + d, hi), m3 = min(m2 + d, hi);
+    const int n1 = reach(m1), n2 = reach(m2), n3 = reach(m3);
+    const int n = n3 >= k ? n3 : n2 >= k ? n2 : n1;
+    if (n3 >= k) lo = m3;
+    else if (n2 >= k) lo = m2, hi = m3;
+    else if (n1 >= k) lo = m1, hi = m2;
+    else hi = m1;
+    if (n >= k && n <= k + slack(k)) break;
   }
   return lo;
 }
@@ -357,9 +383,7 @@ __device__ __forceinline__ Picked pick_row(const LogpArgs& a, int64_t row, Range
       if (q >= g.hi) continue;
       const Chunk s = chunk_of(a, q);
       const Lane l = lane_of<MODE>(s, from % 64);
-      each_of<DT>(a, s, l, fetch<DT, MODE>(a, row, s, l), [&](uint64_t x) {
-        if (x >> 32 >= bound) keep(P, x);
-      });
+      keep_unit<DT, G>(a, s, l, fetch_of<DT, MODE>(P->x[s.r], row, s, l), bound, P);
     }
   }, [&](uint32_t key, auto f) { each_in<DT, MODE>(a, row, g, top, key, f); });
 }
@@ -444,6 +468,7 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
   const Range g = range_of(a, part);
   const float s2 = a.scale * kLog2e;
   const Given y = a.splits > 1 ? Given{kNoToken, 0.0f} : given<DT>(a, row);     // under way with the logits
+  const void* piece = TOP && (int)threadIdx.x < a.p ? a.x.b[threadIdx.x] : nullptr;
   Stat t = none();
   for (int q = g.lo + w * g.step, b = 0; q < g.hi; q += kMore * waves * g.step, ++b) {
     Unit<DT> u[kMore];
@@ -453,6 +478,7 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
     for (int k = 0; k < kMore; ++k) take<DT>(t, most, u[k], s2);
     if (TOP) top[b * G + threadIdx.x] = order_of(most);
   }
+  if (TOP && (int)threadIdx.x < a.p) pool.x[threadIdx.x] = piece;
   t = block_join(t, stats, waves);
   if (!settle(t, s2)) {        // the same in all waves
     __syncthreads();
@@ -474,7 +500,7 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
   const Row r = row_of(t);
   if (a.splits > 1) {
     float* to = part_space(a, row * a.splits + part);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == G - 64) {
       to[0] = t.m;
       to[1] = t.z;
       to[2] = t.w;
@@ -486,7 +512,7 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
       in_order<G>(best, a.top, [&](int rank, uint64_t place) { list[rank] = place; });
     }
   } else {
-    if (threadIdx.x == 0) write_row(a, row, r, y);
+    if (threadIdx.x == G - 64) write_row(a, row, r, y);      // while the first wave looks for the bound
     if constexpr (TOP) {
       const Picked best = pick_row<DT, MODE, G>(a, row, g, a.top, top, &pool);
       in_order<G>(best, a.top, [&](int rank, uint64_t place) { write_top(a, row, r, rank, place); });

@@ -92,10 +92,10 @@ __device__ __forceinline__ void mask_out(Unit<DT>* t, int i) {
   }
 }
 
-// The lane's unit of a chunk as memory holds it.
+// The lane's unit of a chunk, as memory holds it, of the piece at p.
 template <int DT, int MODE>
-__device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s, const Lane& l) {
-  const char* x = static_cast<const char*>(a.x.b[s.r]) + row * s.len * ElemSize<DT>::value;
+__device__ __forceinline__ Unit<DT> fetch_of(const void* p, int64_t row, const Chunk& s, const Lane& l) {
+  const char* x = static_cast<const char*>(p) + row * s.len * ElemSize<DT>::value;
   if constexpr (MODE != kTiny) {
     return load_unit<DT, access_of(MODE)>(x, l.c);
   } else {
@@ -105,7 +105,7 @@ __device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const
 
 template <int DT, int MODE>
 __device__ __forceinline__ Unit<DT> fetch(const VocabArgs& a, int64_t row, const Chunk& s) {
-  return fetch<DT, MODE>(a, row, s, lane_of<MODE>(s));
+  return fetch_of<DT, MODE>(a.x.b[s.r], row, s, lane_of<MODE>(s));
 }
 
 // ... with -inf for what does not count: the first a.full chunks count as a whole.
