@@ -20,13 +20,14 @@
 // Where too many reach the bound (ties), it is raised first, by halving the interval of (logit, column).
 // Few rows are cut into parts, a workgroup each, whose sums and best columns a second launch joins.
 //
-// Large calls are bound by memory: without the exponentials and the sums, 4096 x 131072 take 181 us where they
-// take 188 with them.  Measured on MI355X (GPU time; a copy of 8 GiB runs at 6.55 TB/s, reads alone at 7.0):
-//   4096 x 131072 bfloat16, 8 ranks     182 us, 5.9 TB/s; top 20 184, top 64 207
-//   16384 x 131072                      643 us, 6.7 TB/s: a call's last rows leave the GPU unevenly
-//   1003 x 50017 float32, 9 ranks       35 us, 5.7 TB/s; top 64 44
-//   16 x 128000 bfloat16, top 20        12.5 us in two launches
-//   1 x 32000 float16, top 5            9.5 us in one
+// Large calls are bound by memory, and by the search for the best columns at the end of each row.  Measured on
+// MI355X (GPU time; a copy of 8 GiB runs at 6.55 TB/s, reads alone at 7.0):
+//   4096 x 131072 bfloat16, 8 ranks     158 us, 6.8 TB/s; top 20 185, top 64 197
+//   16384 x 131072                      641 us, 6.7 TB/s
+//   1003 x 50017 float32, 9 ranks       35.5 us, 5.7 TB/s; top 64 45 to 46
+//   16 x 128000 bfloat16, top 20        12.4 us in two launches
+//   1 x 32000 float16, top 5            9.3 us in one
+//   64 x 4096 bfloat16, top 5           7.0 us, of which the search is 3, half of that the second reading
 //   gradient of 4096 x 131072           348 us, 6.2 TB/s
 // It reads 1.05 times the logits' bytes with 20 alternatives of 131072 bfloat16 columns, 1.28 times with 64
 // of 50017 float32 ones (HBM counters): the groups that are read again, a line for each unit.  The gradient reads
@@ -475,7 +476,11 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
     fetch_all<DT, MODE, kMore>(u, a, row, q, waves * g.step, g.hi);
     float most = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kMore; ++k) take<DT>(t, most, u[k], s2);
+    for (int k = 0; k < kMore; ++k) {
+      // short rows: what lies behind them is not computed (16384 x 1024 bfloat16: 28 us, 22.5 so; with more
+      // threads, where few units lie behind a row's end, the branches cost 2%)
+      if (G > 128 || k == 0 || q + k * waves * g.step < g.hi) take<DT>(t, most, u[k], s2);
+    }
     if (TOP) top[b * G + threadIdx.x] = order_of(most);
   }
   if (TOP && (int)threadIdx.x < a.p) pool.x[threadIdx.x] = piece;
@@ -667,8 +672,8 @@ template <int DT, int MODE>
 hipError_t logp_size(const LogpArgs& a, hipStream_t s) {
   if (a.splits > 1) return rows_go<DT, 256, MODE>(a, s);
   // threads to a row: fewer for short rows, of which a compute unit then holds more, and the others' loads
-  // cover a row's end; as many as pay off where rows are too few for that (top 20, us with 512, 256 and 128;
-  // 4096 x 32000: 66, 59, 70; 16384 x 8192: 147, 83, 73; 300 x 32000: 14.3, 15.4, 22.7)
+  // cover a row's end; as many as pay off where rows are too few for that (top 20, us with 512, 256 and 128
+  // before later steps; 4096 x 32000: 66, 59, 70; 16384 x 8192: 147, 83, 73; 300 x 32000: 14.3, 15.4, 22.7)
   const bool many = a.tokens >= 2048;
   if (a.total <= (many ? 16 : 8)) return rows_go<DT, 128, MODE>(a, s);
   return many && a.total <= 128 ? rows_go<DT, 256, MODE>(a, s) : rows_go<DT, 512, MODE>(a, s);
