@@ -305,3 +305,23 @@ def test_results_do_not_depend_on_how_the_vocabulary_is_cut():
     for o in outs:
         B.ra_token_logprobs(logits, y, *o)
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("p,v", [(1, 1000), (3, 20_000), (64, 4001)])
+def test_alternatives_where_nan_or_zeros_make_the_bound(p, v, dt):
+    """As many NaN as alternatives, one fewer, one more, hundreds, all; and zeros of both signs in their place."""
+    require_gpu()
+    k = 20
+    g = torch.Generator(device="cuda").manual_seed(v)
+    counts = (1, k - 1, k, k + 1, 300, v)
+    x = torch.randn((2 * len(counts), v), device="cuda", generator=g).to(T[dt])
+    for i, n in enumerate(counts):
+        at = torch.randperm(v, device="cuda", generator=g)[:n]
+        x[2 * i, at] = math.nan
+        x[2 * i + 1] = -1 - x[2 * i + 1].abs()
+        x[2 * i + 1, at] = torch.where(at % 2 == 0, 0.0, -0.0).to(T[dt])
+    ids = torch.empty((x.shape[0], k), dtype=torch.int64, device="cuda")
+    print(f"[case] bound {p} {v} {dt}", flush=True)
+    B.ra_token_logprobs(cut(x, p, 0), top_ids=ids)
+    assert torch.equal(ids, A.best(x, k))
