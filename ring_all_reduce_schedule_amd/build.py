@@ -77,7 +77,7 @@ def c_check_command(out=C_CHECK_BIN):
 
 C_CHECKS = os.path.join(ROOT, "tests", "c")
 HOST_CHECKS = ["host_check", "host_check_rows"]
-MORE_HOST_CHECKS = ["host_check_answers"]
+MORE_HOST_CHECKS = ["host_check_answers", "host_check_streams"]
 
 
 def host_check_commands(objs, out=C_CHECKS, programs=None):

@@ -221,6 +221,14 @@ constexpr uint32_t kFlagStride = 128;   // > 2(p-1) hops for p <= 64
 std::mutex g_ws_mu;
 std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
 
+// Zeros device memory that kernels on s use next, by a kernel on s.  (hipMemset goes to the null
+// stream, does not wait on the host for device memory, and a non-blocking stream is not ordered
+// behind it: counters cleared that way could be cleared when the first slices had been posted,
+// and the waits for those slices then ran out.)
+hipError_t clear_on(void* p, size_t bytes, hipStream_t s) {
+  return ra::launch_fill_u32(static_cast<uint32_t*>(p), 0u, (int64_t)(bytes / sizeof(uint32_t)), s);
+}
+
 int get_workspace(hipStream_t s, Workspace** out) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -235,8 +243,8 @@ int get_workspace(hipStream_t s, Workspace** out) {
     void* p = nullptr;
     e = hipMalloc(&p, sizeof(ra::WsHeader));
     if (e != hipSuccess) return fail_hip(e, "hipMalloc(workspace)");
-    e = hipMemset(p, 0, sizeof(ra::WsHeader));
-    if (e != hipSuccess) { (void)hipFree(p); return fail_hip(e, "hipMemset(workspace)"); }
+    e = clear_on(p, sizeof(ra::WsHeader), s);
+    if (e != hipSuccess) { (void)hipFree(p); return fail_hip(e, "clearing the workspace"); }
     w.hdr = static_cast<ra::WsHeader*>(p);
   }
   *out = &w;
@@ -259,7 +267,7 @@ int reserve_flags(Workspace* w, int64_t entries, hipStream_t s, bool renew, uint
     const bool wrap = (uint64_t)w->epoch * kFlagStride + kFlagStride >= 0xFFFFFFFFull;
     if (wrap) w->epoch = 1;
     if (renew || wrap) {
-      hipError_t e = ra::launch_fill_u32(w->flags, 0u, w->flag_cap, s);
+      hipError_t e = clear_on(w->flags, (size_t)w->flag_cap * sizeof(uint32_t), s);
       if (e != hipSuccess) return fail_hip(e, "resetting flags");
     }
     *base = w->epoch * kFlagStride;
@@ -284,16 +292,16 @@ int reserve_flags(Workspace* w, int64_t entries, hipStream_t s, bool renew, uint
     void* p = nullptr;
     hipError_t e = hipMalloc(&p, (size_t)cap * sizeof(uint32_t));
     if (e != hipSuccess) return fail_hip(e, "hipMalloc(flags)");
-    e = hipMemset(p, 0, (size_t)cap * sizeof(uint32_t));
-    if (e != hipSuccess) { (void)hipFree(p); return fail_hip(e, "hipMemset(flags)"); }
+    e = clear_on(p, (size_t)cap * sizeof(uint32_t), s);
+    if (e != hipSuccess) { (void)hipFree(p); return fail_hip(e, "clearing flags"); }
     w->flags = static_cast<uint32_t*>(p);
     w->flag_cap = cap;
   }
   // counters only grow: every call starts above anything an earlier call left
   w->epoch += 1;
   if ((uint64_t)w->epoch * kFlagStride + kFlagStride >= 0xFFFFFFFFull) {
-    hipError_t e = hipStreamSynchronize(s);
-    if (e == hipSuccess) e = hipMemset(w->flags, 0, (size_t)w->flag_cap * sizeof(uint32_t));
+    // behind the calls that count in them, which are on s, too
+    hipError_t e = clear_on(w->flags, (size_t)w->flag_cap * sizeof(uint32_t), s);
     if (e != hipSuccess) return fail_hip(e, "resetting flags");
     w->epoch = 1;
   }
@@ -642,8 +650,10 @@ int ra_stream_status(hipStream_t stream) {
     e = hipMemcpy(&status, &hdr->status, sizeof status, hipMemcpyDeviceToHost);
     if (e != hipSuccess) return fail_hip(e, "reading device status");
     if (status == 0) continue;
-    // clear the sticky error and the barrier words the aborted kernel left behind
-    e = hipMemset(hdr, 0, sizeof(ra::WsHeader));
+    // clear the sticky error and the barrier words the aborted kernel left behind, and wait: the
+    // scratch's next call may be on another stream
+    e = clear_on(hdr, sizeof(ra::WsHeader), stream);
+    if (e == hipSuccess) e = hipStreamSynchronize(stream);
     if (e != hipSuccess) return fail_hip(e, "clearing device status");
     return fail((int)status, "a device-side wait timed out (status %u)", status);
   }
