@@ -107,6 +107,17 @@ __device__ __forceinline__ bool settle(Stat& t, float s2) {
   return good;
 }
 
+// Differences of logits to exponents of 2: x s log2 e.  The product s log2 e leaves float32 for an s beyond
+// 2.3 10^38 (0 times it would be NaN, and all rows are settled by the difference then): s goes first there.
+struct Exponent {
+  float s, more;
+  __device__ __forceinline__ float operator()(float x) const { return x * s * more; }
+};
+__device__ __forceinline__ Exponent exponent_of(float scale) {
+  const float s2 = scale * kLog2e;
+  return s2 < INFINITY ? Exponent{s2, 1.0f} : Exponent{scale, kLog2e};
+}
+
 // The chunks of a workgroup: lo, lo + step, ... below hi, its waves taking one each in turn.  The parts of
 // a row take turns, too: the last chunks, which are short where pieces end in them, go to many.
 struct Range {
@@ -116,7 +127,8 @@ __device__ __forceinline__ Range range_of(const VocabArgs& a, int part) { return
 
 // The statistics of a range with the largest logit subtracted first, by the workgroup.
 template <int DT, int MODE>
-__device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range g, float s2, float* lds) {
+__device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range g, float* lds) {
+  const Exponent exponent = exponent_of(a.scale);
   const int w = wave_id(), waves = blockDim.x / 64;
   float m = -INFINITY;
   for (int q = g.lo + w * g.step; q < g.hi; q += waves * g.step) {
@@ -138,7 +150,7 @@ __device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range
     fetch_all<DT, MODE, 1>(u, a, row, q, waves * g.step, g.hi);
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const float y = (unit_get<DT>(u[0], i) - at) * s2, e = exp2_of(y);
+      const float y = exponent(unit_get<DT>(u[0], i) - at), e = exp2_of(y);
       z += e;
       v = __builtin_fmaf(e, __builtin_fmaxf(y, kFloor), v);
     }
@@ -487,7 +499,7 @@ __global__ __launch_bounds__(G) void k_logp(LogpArgs a) {
   t = block_join(t, stats, waves);
   if (!settle(t, s2)) {        // the same in all waves
     __syncthreads();
-    t = plain_stat<DT, MODE>(a, row, g, s2, reinterpret_cast<float*>(stats));
+    t = plain_stat<DT, MODE>(a, row, g, reinterpret_cast<float*>(stats));
     if (TOP && t.z != t.z) {
       // the maxima passed over NaN, which is the largest
       for (int q = g.lo + w * g.step, b = 0; q < g.hi; q += kMore * waves * g.step, ++b) {
@@ -554,9 +566,9 @@ __global__ __launch_bounds__(TOP ? kJoinThreads : 64) void k_logp_join(LogpArgs 
     }
   }
   // every wave for itself
-  const float s2 = a.scale * kLog2e, m = wave_max(t.m);
+  const float m = wave_max(t.m);
   // NaN (of -inf - -inf) becomes the floor, too
-  const float d = __builtin_fmaxf((t.m - m) * s2, kFloor), r = exp2_of(d);
+  const float d = __builtin_fmaxf(exponent_of(a.scale)(t.m - m), kFloor), r = exp2_of(d);
   const Row all = row_of({m, 0.0f, wave_sum(r * t.z), wave_sum(r * __builtin_fmaf(d, t.z, t.w))});
   if (threadIdx.x == 0) write_row(a, row, all, y);
   if constexpr (TOP) {
