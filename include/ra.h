@@ -536,7 +536,9 @@ int ra_cross_entropy_backward(void* const* logits, int p, int64_t tokens, int64_
  *   top      0..64, at most `valid`
  *   top_ids, top_logprobs  [tokens][top] of id_dtype, and float32: the columns with the
  *            largest logits, largest first, and of equal ones the lowest column first; with
- *            their log probabilities.  Either may be NULL.
+ *            their log probabilities.  Either may be NULL.  (Rows with fewer than `top` columns above
+ *            -inf, or with thousands of equal logits at the last one's place, are searched in some
+ *            twenty readings of the row in place of one.)
  *   workspace  ra_token_logprobs_workspace bytes
  * Logits of -inf are masked columns: they come last.  A row all of whose columns are -inf
  * has lse = -inf, entropy 0 and log probabilities of -inf.  A logit of +inf or NaN makes
@@ -558,7 +560,8 @@ int ra_token_logprobs_workspace(int64_t tokens, int64_t vocab, int p, int top, i
  *   grads    p arrays like logits; grads[r] may be logits[r]
  * A token whose two gradients are 0 gets zeros whatever its logits hold, and so does one
  * whose lse is -inf (all of its columns are).  An id from `valid` on, or an lse of +inf or NaN, makes
- * the token's gradient NaN.  Columns from `valid` on get zeros.
+ * the token's gradient NaN.  Columns from `valid` on get zeros.  scale times a gradient has to be within
+ * float32.
  */
 int ra_token_logprobs_backward(void* const* logits, int p, int64_t tokens, int64_t vocab, int64_t valid,
                                int dtype, float scale, const void* ids, int id_dtype, const float* lse,
@@ -644,7 +647,9 @@ int ra_grad_clip(void* const* tensors, const int64_t* counts, const int* dtypes,
  * ra_allreduce_clip -- an all-reduce of gradients and ra_grad_clip of its result, to the ranks:
  *     g = sum_r bufs[r]  (RA_AVG: that divided by p), rounded to `dtype`
  *     norm = scale sqrt(sum g^2),   c = scale min(1, max_norm / (norm + 1e-6)),   out = g c
- * The ranks' buffers are added in rank order, 0 first, in float32.
+ * The ranks' buffers are added in rank order, 0 first, in float32.  The norm is that of this one buffer:
+ * gradients that come in several buckets go through ra_allreduce bucket by bucket, and then through one
+ * ra_grad_clip of a list that has rank 0's buckets first (`counted` of them) and the other ranks' behind them.
  *   bufs   p arrays of n elements of `dtype` (n up to 2^40)
  *   op     RA_SUM or RA_AVG
  *   outs   n_out (1..p) arrays like bufs; each may be one of bufs

@@ -843,8 +843,8 @@ def ra_grad_clip(tensors, max_norm, norm, outs=None, counted=None, scale=1.0, wo
 def ra_allreduce_clip(bufs, max_norm, norm, outs=None, op="avg", scale=1.0, workspace=None,
                       stream=None):
     """The ranks' buffers averaged (op "avg") or added ("sum"), scaled so that their norm is at
-    most max_norm, into outs (None: in place); see include/ra.h.  norm, one float32, gets the
-    norm before."""
+    most max_norm, into outs (None: in place); see include/ra.h, also for gradients in more buffers
+    than one a rank.  norm, one float32, gets the norm before."""
     ptrs, p, n, code, _ = _marshal(bufs)
     b0 = _list(bufs)[0]
     dev = b0.get_device()

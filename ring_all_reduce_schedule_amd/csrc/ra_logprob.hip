@@ -22,7 +22,10 @@
 //
 // Large calls are bound by memory, and by the search for the best columns at the end of each row.  Measured on
 // MI355X (GPU time; a copy of 8 GiB runs at 6.55 TB/s, reads alone at 7.0):
-//   4096 x 131072 bfloat16, 8 ranks     158 to 179 us from card to card, 6.0 to 6.8 TB/s; top 20 185, top 64 197
+//   4096 x 131072 bfloat16, 8 ranks     158 to 179 us from card to card and from buffers to buffers, 6.0 to 6.8 TB/s;
+//                                       top 20 172 to 185, top 64 197
+//   the same with three columns left in every row, or all of them equal, top 20   5.9 ms: 22 halvings and a reading
+//                                       of the row for each; 16 x 128000 262 us, 1 x 32000 300
 //   16384 x 131072                      641 us, 6.7 TB/s
 //   1003 x 50017 float32, 9 ranks       35.5 us, 5.7 TB/s; top 64 45 to 46
 //   16 x 128000 bfloat16, top 20        12.4 us in two launches
