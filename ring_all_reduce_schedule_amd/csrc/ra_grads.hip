@@ -55,7 +55,9 @@ __device__ __forceinline__ double parts_sum(const double* part, int n, double* l
 }
 
 // g times the factor is g hi lo; lo is 1, or 2^-96 where the factor itself would be near
-// float32's end (and hi 2^96 times as large: g hi stays below 2^124).
+// float32's end (and hi 2^96 times as large: g hi stays below 2^124), or 2^-126 where that
+// would be, too (and g hi stays below 2^32).  Such factors belong to gradients near float32's
+// other end, which they bring back into its range.
 struct Factor {
   float norm, hi, lo;
 };
@@ -66,6 +68,7 @@ __device__ __forceinline__ Factor factor_of(double total, const ClipRule& r) {
   const double norm = (double)r.scale * __builtin_sqrt(total);
   const double q = (double)r.max_norm / (norm + 1e-6);
   const double c = (double)r.scale * (q > 1.0 ? 1.0 : q);      // NaN stays
+  if (c < 0x1p-222) return {(float)norm, (float)(c * 0x1p126), 0x1p-126f};
   if (c < 0x1p-100) return {(float)norm, (float)(c * 0x1p96), 0x1p-96f};
   return {(float)norm, (float)c, 1.0f};
 }
