@@ -110,11 +110,18 @@ __device__ __forceinline__ bool settle(Stat& t, float s2) {
   return good;
 }
 
-// Differences of logits to exponents of 2: x s log2 e.  The product s log2 e leaves float32 for an s beyond
+// s (x - m) for x <= m.  The difference of logits near both of float32's ends is beyond it, s times it
+// perhaps not: those are multiplied first, |m s| being at most s (m - x) then.
+__device__ __forceinline__ float below(float x, float m, float s) {
+  const float d = x - m;
+  return d == -INFINITY && x != -INFINITY ? __builtin_fmaf(x, s, -(m * s)) : d * s;
+}
+
+// The same as exponents of 2, s log2 e (x - m).  The product s log2 e leaves float32 for an s beyond
 // 2.3 10^38 (0 times it would be NaN, and all rows are settled by the difference then): s goes first there.
 struct Exponent {
   float s, more;
-  __device__ __forceinline__ float operator()(float x) const { return x * s * more; }
+  __device__ __forceinline__ float operator()(float x, float m) const { return below(x, m, s) * more; }
 };
 __device__ __forceinline__ Exponent exponent_of(float scale) {
   const float s2 = scale * kLog2e;
@@ -153,7 +160,7 @@ __device__ __forceinline__ Stat plain_stat(const LogpArgs& a, int64_t row, Range
     fetch_all<DT, MODE, 1>(u, a, row, q, waves * g.step, g.hi);
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
-      const float y = exponent(unit_get<DT>(u[0], i) - at), e = exp2_of(y);
+      const float y = exponent(unit_get<DT>(u[0], i), at), e = exp2_of(y);
       z += e;
       v = __builtin_fmaf(e, __builtin_fmaxf(y, kFloor), v);
     }
@@ -428,7 +435,7 @@ struct Row {
 __device__ __forceinline__ Row row_of(const Stat& t) { return {t.m, log2_of(t.z) * kLn2, t.z, t.w}; }
 __device__ __forceinline__ bool empty(const Row& t) { return t.m == -INFINITY && t.z == 0.0f; }
 __device__ __forceinline__ float log_p(const Row& t, float x, float scale) {
-  return empty(t) ? -INFINITY : (x - t.m) * scale - t.ln_z;
+  return empty(t) ? -INFINITY : below(x, t.m, scale) - t.ln_z;
 }
 
 // The given token's logit and its column, or what there is instead: kNoToken, kNoColumn.
@@ -571,7 +578,7 @@ __global__ __launch_bounds__(TOP ? kJoinThreads : 64) void k_logp_join(LogpArgs 
   // every wave for itself
   const float m = wave_max(t.m);
   // NaN (of -inf - -inf) becomes the floor, too
-  const float d = __builtin_fmaxf(exponent_of(a.scale)(t.m - m), kFloor), r = exp2_of(d);
+  const float d = __builtin_fmaxf(exponent_of(a.scale)(t.m, m), kFloor), r = exp2_of(d);
   const Row all = row_of({m, 0.0f, wave_sum(r * t.z), wave_sum(r * __builtin_fmaf(d, t.z, t.w))});
   if (threadIdx.x == 0) write_row(a, row, all, y);
   if constexpr (TOP) {
