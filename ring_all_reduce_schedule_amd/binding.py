@@ -764,10 +764,10 @@ class TensorList:
     ra_grad_norm and ra_grad_clip, which accept one in place of a list of tensors or a
     RankBuffers.  It holds references to the tensors, which must not be resized or re-pointed
     (``resize_``, ``set_``, ``.data =``) meanwhile: the table holds the addresses they had when it
-    was made, and a call raises if any tensor's address or length has changed.  Looking at them costs about 0.09 us of
-    host time a tensor, checking and marshalling a list 0.3: the norm of 75 tensors takes 17 us of it a
-    call with this and 33 with a list.  (A loop whose gradients are new tensors in every step has
-    to make a new TensorList, or to pass the list.)"""
+    was made, and a call raises if any tensor's address or length has changed.  Looking at them
+    costs about 0.09 us of host time a tensor, checking and marshalling a list 0.3: the norm of 75
+    tensors takes 17 us of it a call with this and 33 with a list.  (A loop whose gradients are
+    new tensors in every step has to make a new TensorList, or to pass the list.)"""
 
     __slots__ = ("tensors", "device", "_ptrs", "_counts", "_codes", "_addresses", "_lengths")
 
